@@ -351,6 +351,190 @@ int dsa_abi_version(void);
  * the difference across a region counts the library's kernels in it. */
 uint64_t dsa_launch_count(void);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit latent cache.
+ *
+ * The method caches one 576-wide latent row per token; at 1152 bytes of bf16 it is
+ * the larger part of what a long context holds.  These calls keep the row in
+ * 8 bits: E4M3 codes with one fp32 scale for every block of tokens (the latent
+ * cache of the MQA form has a single key/value head, so a block of tokens and a
+ * head is a block of tokens; the 8-bit format is the one the method uses for the
+ * indexer, "DeepSeek 稀疏注意力路线", section "工程要点").
+ *   kv8   (device) E4M3 bytes [kv_rows, 576]
+ *   scale (device) fp32 [ceil(kv_rows / scale_block)]: cache row r holds the values
+ *         scale[r / scale_block] * kv8[r, :]
+ *   scale_block  tokens per scale: 1, 2, 4, 8, 16, 32 or 64
+ * Rows are found as in dsa_batch (contiguous or paged); r is the physical row, so
+ * a page holds whole blocks.
+ */
+
+/* Further bit flags of the device status word. */
+#define DSA_DEV_BAD_SCALE 16u     /* a scale outside [2^-100, 2^100] (or NaN); its rows were skipped */
+#define DSA_DEV_NO_PAGES 32u      /* dsa_pages_resize: too few free pages; no sequence grew */
+
+/* Operation codes for dsa_q8_workspace_size. */
+#define DSA_Q8_APPEND 0
+#define DSA_Q8_MLA 1
+#define DSA_Q8_FORWARD 2
+#define DSA_Q8_PROJECT 3
+
+/* Bytes of workspace an 8-bit-cache operation needs (>= 256: the status word lies
+ * at its start).  k = 0 with DSA_Q8_MLA asks for the dense form (idx = NULL).
+ * Returns 0 for an invalid op, batch, H_I, H or k.  H_I is read by
+ * DSA_Q8_FORWARD and DSA_Q8_PROJECT, H by all but DSA_Q8_APPEND. */
+size_t dsa_q8_workspace_size(int op, const dsa_batch *batch, int H_I, int H, int k);
+
+/*
+ * Appends latent rows to the 8-bit cache.
+ *   kv (device) bf16 bits [T, 576]: the latent row of each new token; token t goes
+ *      to the cache row of position q_pos[t] of sequence q_seq[t]
+ * Order: the tokens come sequence by sequence (q_seq ascending) with consecutive
+ * ascending positions within a sequence.  For each block of scale_block positions
+ * that receives tokens,
+ *   need  = 2^e, e the smallest integer >= -100 with 448 * 2^e >= the largest
+ *           finite |entry| of the block's new rows (at most 100)
+ *   scale = need where the block's first position is among the new tokens, else
+ *           max(scale, need): rows that the block held before (its positions below
+ *           the first new one) are re-encoded when the scale grows
+ *   kv8   = E4M3(kv / scale), round to nearest even, saturating at +-448
+ * Scales are thus powers of two: dividing by one is exact, and a re-encoded row
+ * loses only what falls below E4M3's smallest step (2^-9 of the scale).
+ * Infinite entries saturate, NaN stays NaN.  No other row or scale is written.
+ * A token outside its sequence, or a contiguous sequence whose kv_offset is not a
+ * multiple of scale_block, raises DSA_DEV_BAD_QUERY and is not appended; one whose
+ * cache row lies outside kv_rows raises DSA_DEV_BAD_INDEX; a block's earlier scale
+ * outside [2^-100, 2^100] raises DSA_DEV_BAD_SCALE (need is taken and the earlier
+ * codes stay).  Tokens out of order raise DSA_DEV_BAD_QUERY; the rows of the
+ * sequences concerned are then unspecified.
+ * Two sequences may share pages (dsa_pages_fork) as long as neither appends to a
+ * page they share: let dsa_pages_resize grow them first.
+ * Workspace: DSA_Q8_APPEND.  Supported: kv, kv8 and ws 16-byte aligned.
+ */
+dsa_status dsa_quantize_append(const dsa_batch *batch, const uint16_t *kv, uint8_t *kv8, float *scale,
+                               int scale_block, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * dsa_project_append with an 8-bit latent cache: the tokens' latent rows (rounded
+ * to bf16 as dsa_project_append stores them) go through dsa_quantize_append into
+ * kv8 and scale; everything else is as in dsa_project_append.  The order of the
+ * tokens and the flags are those of both calls.  Workspace: DSA_Q8_PROJECT.
+ */
+dsa_status dsa_project_append_q8(const dsa_batch *batch, const uint16_t *hidden, const uint16_t *w_all, int d_model,
+                                 int H_I, int H, float rope_base, uint8_t *q_idx, float *w, uint16_t *q,
+                                 uint8_t *k_idx, uint8_t *kv8, float *scale, int scale_block, void *ws,
+                                 size_t ws_bytes, void *stream);
+
+/*
+ * Sparse MLA over the 8-bit cache: dsa_sparse_mla with row r's key and value
+ * scale[r / scale_block] * kv8[r, :].
+ *   idx (device) int32 [T, k] as in dsa_sparse_mla, or NULL with k = 0: the dense
+ *       form, every visible key 0 .. q_pos[t] of any context length
+ * The cache's codes are the tensor cores' operand as they are; the bf16 queries and
+ * the softmax weights (times their rows' scales) enter as sums of two E4M3 numbers,
+ * which hold 8 significant bits like bf16.  Per query and head the weights are held
+ * relative to the largest p_i * scale_i, to 2^-18 of it absolutely, and the
+ * query's entries relative to its largest one, to 2^-18.  fp32 logits, softmax
+ * statistics and sums.  A query row with an infinite or NaN entry gives NaN, and so
+ * does a selected row with a NaN code.
+ * A row whose scale is outside [2^-100, 2^100] raises DSA_DEV_BAD_SCALE and is
+ * skipped.  In the dense form a query position outside its sequence raises
+ * DSA_DEV_BAD_QUERY; such a query, and one with no usable row, gets out = 0 and
+ * lse = -inf.
+ * Workspace: DSA_Q8_MLA.  Supported: H and k as in dsa_sparse_mla; q, kv8, out and
+ * ws 16-byte aligned, sm_scale finite.
+ */
+dsa_status dsa_sparse_mla_q8(const dsa_batch *batch, const uint16_t *q, const uint8_t *kv8, const float *scale,
+                             int scale_block, const int32_t *idx, int k, int H, float sm_scale, uint16_t *out,
+                             float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* dsa_forward over the 8-bit cache: indexer, top-k and dsa_sparse_mla_q8 on one
+ * stream, scores and selected indices in `ws`.  Workspace: DSA_Q8_FORWARD. */
+dsa_status dsa_forward_q8(const dsa_batch *batch, const uint8_t *q_idx, const uint8_t *k_idx, const float *w, int H_I,
+                          const uint16_t *q, const uint8_t *kv8, const float *scale, int scale_block, int H, int k,
+                          float sm_scale, uint16_t *out, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Pages of a paged cache.
+ *
+ * A pool of num_pages physical pages of page_size rows is shared by num_seqs
+ * sequences.  page_table and seq_len have the layout that dsa_batch reads (its
+ * page_table and kv_len), so a batch can point at them.
+ *   page_table (device) int32 [num_seqs, pages_per_seq]: the physical page of each
+ *              page of a sequence; the first ceil(seq_len / page_size) entries count
+ *   seq_len    (device) int32 [num_seqs]: rows that the sequence holds
+ *   ref_count  (device) int32 [num_pages]: sequences that hold the page, 0 = free
+ * Every call reads the state `in` and writes the whole of the state `out`: the same
+ * three arrays (in place), or three others that share no memory with them.  Sizes
+ * of both are equal.  Entries of `out` that the call does not change equal those of
+ * `in`.  The results depend on the input alone (no order of threads shows).
+ */
+typedef struct dsa_page_state {
+  int32_t num_seqs;        /* >= 1 */
+  int32_t num_pages;       /* >= 1 */
+  int32_t page_size;       /* rows per page: a multiple of 64 */
+  int32_t pages_per_seq;   /* >= 1; pages_per_seq * page_size < 2^31 */
+  int32_t *page_table;
+  int32_t *seq_len;
+  int32_t *ref_count;
+} dsa_page_state;
+
+/* The buffers whose pages move with a pool's pages (latent rows, their scales,
+ * indexer keys ...): page p of buffer j is the page_bytes[j] bytes at
+ * base[j] + p * page_bytes[j].  4-byte aligned, page_bytes multiples of 4. */
+#define DSA_MAX_PAGE_BUFFERS 8
+typedef struct dsa_page_buffers {
+  int32_t num;                                  /* 0 .. DSA_MAX_PAGE_BUFFERS */
+  void *base[DSA_MAX_PAGE_BUFFERS];             /* (device) */
+  int64_t page_bytes[DSA_MAX_PAGE_BUFFERS];
+} dsa_page_buffers;
+
+/* Bytes of workspace of the three calls below for lists of up to n entries; 0 for an
+ * invalid state or a negative n. */
+size_t dsa_pages_workspace_size(const dsa_page_state *state, int n);
+
+/*
+ * Sets the lengths of n sequences: allocates the pages of those that grow, gives
+ * back the pages behind those that shrink (new_len 0 frees a sequence).
+ *   seqs, new_len (device) int32 [n]: seq_len[seqs[i]] becomes new_len[i]
+ * First every entry that shrinks drops its pages behind the new length (the page's
+ * ref_count falls by one, the table entry becomes -1).  Then the growing entries,
+ * in the order of the list, take the lowest free pages (ref_count becomes 1) for
+ * the pages they lack.  A growing sequence whose last page is partly filled and
+ * held by others too gets a copy of it first (copy on write: a free page, all
+ * buffers' bytes copied, the old page's ref_count falls by one); of several growing
+ * sequences that share a page and no one else holds, the last one keeps it.
+ * When there are too few free pages for all growing entries none of them grows
+ * (DSA_DEV_NO_PAGES).  An entry with a sequence or length out of range, or one
+ * that names a sequence that an earlier entry names, is skipped
+ * (DSA_DEV_BAD_QUERY); table entries outside the pool raise DSA_DEV_BAD_INDEX and
+ * are left alone (such a page is not dropped, nor copied).
+ *   buffers may be NULL (no data to copy)
+ */
+dsa_status dsa_pages_resize(const dsa_page_state *in, const dsa_page_state *out, int n, const int32_t *seqs,
+                            const int32_t *new_len, const dsa_page_buffers *buffers, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/*
+ * Forks n sequences: dst_seqs[i] gets the length and the pages of src_seqs[i]
+ * (ref_count rises; no data is copied until one of them grows into a shared page,
+ * see dsa_pages_resize).  A pair with an index out of range, a destination that
+ * holds rows or that an earlier pair names, or a source that is some pair's
+ * destination is skipped (DSA_DEV_BAD_QUERY).
+ */
+dsa_status dsa_pages_fork(const dsa_page_state *in, const dsa_page_state *out, int n, const int32_t *src_seqs,
+                          const int32_t *dst_seqs, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Compacts the pool: with L pages in use, the pages in use at L and above move, in
+ * ascending order, to the free pages below L, so that pages 0 .. L-1 are the ones in
+ * use.  Data, page_table and ref_count follow; seq_len stays.
+ *   page_map (device, may be NULL) int32 [num_pages]: the new place of each page that
+ *            was in use, -1 for a free one
+ * The bytes of the pages that were moved away stay as they were.
+ */
+dsa_status dsa_pages_compact(const dsa_page_state *in, const dsa_page_state *out, const dsa_page_buffers *buffers,
+                             int32_t *page_map, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,3 +8,4 @@ from .dsa_ref import (attention_probs, bf16_decode, bf16_encode_rne, dense_mla, 
                       topk_select)
 from . import projection  # noqa: F401,E402
 from . import backward  # noqa: F401,E402
+from . import cache  # noqa: F401,E402

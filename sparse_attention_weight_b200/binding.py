@@ -21,13 +21,19 @@ DSA_OK = 0
 STATUS_NAMES = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARGUMENT", 2: "DSA_ERR_UNSUPPORTED",
                 3: "DSA_ERR_WORKSPACE_TOO_SMALL", 4: "DSA_ERR_CUDA", 5: "DSA_ERR_DEVICE"}
 DEV_BAD_QUERY, DEV_BAD_INDEX, DEV_TIMEOUT = 1, 2, 4
+DEV_BAD_SCALE, DEV_NO_PAGES = 16, 32
 OP_INDEXER, OP_TOPK, OP_SPARSE_MLA, OP_FORWARD, OP_PROJECT, OP_MLA_BACKWARD, OP_FORWARD_HOST = 0, 1, 2, 3, 4, 5, 6
+# operations of the 8-bit latent cache (dsa_q8_workspace_size)
+Q8_APPEND, Q8_MLA, Q8_FORWARD, Q8_PROJECT = 0, 1, 2, 3
+MAX_PAGE_BUFFERS = 8
 
 EXPORTS = ("dsa_workspace_size", "dsa_indexer_scores", "dsa_topk", "dsa_sparse_mla", "dsa_forward",
            "dsa_forward_ws_views", "dsa_read_device_status", "dsa_status_string", "dsa_abi_version",
            "dsa_indexer_scores_noalloc", "dsa_selftest_wait_timeout", "dsa_launch_count", "dsa_project_append",
            "dsa_indexer_scores_hist", "dsa_topk_hist", "dsa_topk_uses_hist", "dsa_sparse_mla_backward",
-           "dsa_forward_host")
+           "dsa_forward_host", "dsa_q8_workspace_size", "dsa_quantize_append", "dsa_project_append_q8",
+           "dsa_sparse_mla_q8", "dsa_forward_q8", "dsa_pages_workspace_size", "dsa_pages_resize", "dsa_pages_fork",
+           "dsa_pages_compact")
 NOALLOC_MAX_Q = 16384
 
 
@@ -47,6 +53,17 @@ class DsaBatch(ctypes.Structure):
                 ("kv_offset", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("q_seq", ctypes.c_void_p),
                 ("q_pos", ctypes.c_void_p), ("page_size", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
                 ("page_table", ctypes.c_void_p)]
+
+
+class DsaPageState(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("ref_count", ctypes.c_void_p)]
+
+
+class DsaPageBuffers(ctypes.Structure):
+    _fields_ = [("num", ctypes.c_int32), ("base", ctypes.c_void_p * MAX_PAGE_BUFFERS),
+                ("page_bytes", ctypes.c_int64 * MAX_PAGE_BUFFERS)]
 
 
 _lib = None
@@ -76,6 +93,18 @@ def lib() -> ctypes.CDLL:
         L.dsa_forward_host.argtypes = [bp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp,
                                        vp, sz, ctypes.POINTER(vp)]
         L.dsa_topk_uses_hist.restype = i32
+        sp, pp = ctypes.POINTER(DsaPageState), ctypes.POINTER(DsaPageBuffers)
+        L.dsa_q8_workspace_size.argtypes = [i32, bp, i32, i32, i32]
+        L.dsa_q8_workspace_size.restype = sz
+        L.dsa_quantize_append.argtypes = [bp, vp, vp, vp, i32, vp, sz, vp]
+        L.dsa_project_append_q8.argtypes = [bp, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+        L.dsa_sparse_mla_q8.argtypes = [bp, vp, vp, vp, i32, vp, i32, i32, f32, vp, vp, vp, sz, vp]
+        L.dsa_forward_q8.argtypes = [bp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, sz, vp]
+        L.dsa_pages_workspace_size.argtypes = [sp, i32]
+        L.dsa_pages_workspace_size.restype = sz
+        L.dsa_pages_resize.argtypes = [sp, sp, i32, vp, vp, pp, vp, sz, vp]
+        L.dsa_pages_fork.argtypes = [sp, sp, i32, vp, vp, vp, sz, vp]
+        L.dsa_pages_compact.argtypes = [sp, sp, pp, vp, vp, sz, vp]
         L.dsa_selftest_wait_timeout.argtypes = [vp, sz, ctypes.c_uint32, vp]
         L.dsa_forward_ws_views.argtypes = [bp, i32, i32, i32, vp, ctypes.POINTER(vp), ctypes.POINTER(i64),
                                            ctypes.POINTER(vp)]
@@ -87,7 +116,8 @@ def lib() -> ctypes.CDLL:
         for fn in ("dsa_indexer_scores", "dsa_topk", "dsa_sparse_mla", "dsa_forward", "dsa_forward_ws_views",
                    "dsa_read_device_status", "dsa_indexer_scores_noalloc", "dsa_selftest_wait_timeout",
                    "dsa_project_append", "dsa_indexer_scores_hist", "dsa_topk_hist", "dsa_sparse_mla_backward",
-                   "dsa_forward_host"):
+                   "dsa_forward_host", "dsa_quantize_append", "dsa_project_append_q8", "dsa_sparse_mla_q8",
+                   "dsa_forward_q8", "dsa_pages_resize", "dsa_pages_fork", "dsa_pages_compact"):
             getattr(L, fn).restype = i32
         _lib = L
     return _lib
@@ -148,6 +178,66 @@ class DeviceBatch:
         return cls(off, ln, qs, qp, st, pt)
 
 
+    @classmethod
+    def from_pages(cls, state: "PageState", q_seq: torch.Tensor, q_pos: torch.Tensor, max_kv_len: int,
+                   max_q_per_seq: int = 0) -> "DeviceBatch":
+        """A paged batch over a pool: its page table and lengths are the state's own
+        arrays, so the batch follows what the page calls write into them."""
+        for t in (q_seq, q_pos):
+            if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != q_seq.numel():
+                raise ValueError("q_seq and q_pos must be contiguous int32 tensors of one length")
+        st = DsaBatch(state.struct.num_seqs, q_seq.numel(), max_kv_len, max_q_per_seq,
+                      state.struct.num_pages * state.struct.page_size, None, state.seq_len.data_ptr(),
+                      q_seq.data_ptr(), q_pos.data_ptr(), state.struct.page_size, state.struct.pages_per_seq,
+                      state.page_table.data_ptr())
+        return cls(None, state.seq_len, q_seq, q_pos, st, state.page_table)
+
+
+class PageState:
+    """The page table [num_seqs, pages_per_seq], lengths [num_seqs] and reference counts
+    [num_pages] of a pool (int32 device tensors, kept by reference) and their struct."""
+
+    def __init__(self, page_table: torch.Tensor, seq_len: torch.Tensor, ref_count: torch.Tensor, page_size: int):
+        for t, dims in ((page_table, 2), (seq_len, 1), (ref_count, 1)):
+            if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
+                raise ValueError("a page state holds contiguous int32 tensors [seqs, pages], [seqs] and [pages]")
+        if seq_len.numel() != page_table.shape[0]:
+            raise ValueError("page_table and seq_len disagree about the number of sequences")
+        self.page_table, self.seq_len, self.ref_count = page_table, seq_len, ref_count
+        self.struct = DsaPageState(page_table.shape[0], ref_count.numel(), page_size, page_table.shape[1],
+                                   page_table.data_ptr(), seq_len.data_ptr(), ref_count.data_ptr())
+
+    @classmethod
+    def empty(cls, num_seqs: int, num_pages: int, page_size: int, pages_per_seq: int, device="cuda") -> "PageState":
+        """A pool with every page free."""
+        return cls(torch.full((num_seqs, pages_per_seq), -1, dtype=torch.int32, device=device),
+                   torch.zeros(num_seqs, dtype=torch.int32, device=device),
+                   torch.zeros(num_pages, dtype=torch.int32, device=device), page_size)
+
+    def like(self) -> "PageState":
+        """Another state of the same sizes, to be written by a page call."""
+        return PageState(torch.empty_like(self.page_table), torch.empty_like(self.seq_len),
+                         torch.empty_like(self.ref_count), self.struct.page_size)
+
+
+class PageBuffers:
+    """Cache buffers whose pages move with a pool's pages: each tensor holds num_pages
+    equal parts, page after page."""
+
+    def __init__(self, tensors, num_pages: int):
+        self.tensors = list(tensors)
+        if len(self.tensors) > MAX_PAGE_BUFFERS:
+            raise ValueError(f"at most {MAX_PAGE_BUFFERS} page buffers")
+        self.struct = DsaPageBuffers()
+        self.struct.num = len(self.tensors)
+        for j, t in enumerate(self.tensors):
+            n = t.numel() * t.element_size()
+            if n % num_pages:
+                raise ValueError("a page buffer holds a whole number of bytes per page")
+            self.struct.base[j] = _ptr(t)
+            self.struct.page_bytes[j] = n // num_pages
+
+
 def workspace_size(op: int, batch: DeviceBatch, H_I: int = 64, H: int = 128, k: int = 2048, ld: int = 0) -> int:
     n = lib().dsa_workspace_size(op, ctypes.byref(batch.struct), H_I, H, k, ld)
     if n == 0:
@@ -158,6 +248,23 @@ def workspace_size(op: int, batch: DeviceBatch, H_I: int = 64, H: int = 128, k: 
 def workspace(op: int, batch: DeviceBatch, H_I: int = 64, H: int = 128, k: int = 2048, ld: int = 0,
               device="cuda") -> torch.Tensor:
     return torch.empty(workspace_size(op, batch, H_I, H, k, ld), dtype=torch.uint8, device=device)
+
+
+def q8_workspace(op: int, batch: DeviceBatch, H_I: int = 64, H: int = 128, k: int = 2048,
+                 device="cuda") -> torch.Tensor:
+    """Workspace of an operation of the 8-bit cache (Q8_APPEND, Q8_MLA, Q8_FORWARD, Q8_PROJECT)."""
+    n = lib().dsa_q8_workspace_size(op, ctypes.byref(batch.struct), H_I, H, k)
+    if n == 0:
+        raise DsaError("dsa_q8_workspace_size", 1)
+    return torch.empty(int(n), dtype=torch.uint8, device=device)
+
+
+def pages_workspace(state: PageState, n: int, device="cuda") -> torch.Tensor:
+    """Workspace of the page calls for lists of up to n entries."""
+    size = lib().dsa_pages_workspace_size(ctypes.byref(state.struct), n)
+    if size == 0:
+        raise DsaError("dsa_pages_workspace_size", 1)
+    return torch.empty(int(size), dtype=torch.uint8, device=device)
 
 
 def _check(fn: str, status: int):
@@ -236,6 +343,67 @@ def dsa_forward(batch: DeviceBatch, q_idx, k_idx, w, H_I: int, q, kv, H: int, k:
     _check("dsa_forward", lib().dsa_forward(
         ctypes.byref(batch.struct), _ptr(q_idx), _ptr(k_idx), _ptr(w), H_I, _ptr(q), _ptr(kv), H, k, sm_scale,
         _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def dsa_quantize_append(batch: DeviceBatch, kv, kv8, scale, scale_block: int, ws, stream=None):
+    _check("dsa_quantize_append", lib().dsa_quantize_append(
+        ctypes.byref(batch.struct), _ptr(kv), _ptr(kv8), _ptr(scale), scale_block, _ptr(ws), ws.numel(),
+        _stream(stream)))
+
+
+def dsa_project_append_q8(batch: DeviceBatch, hidden, w_all, d_model: int, H_I: int, H: int, rope_base: float, q_idx,
+                          w, q, k_idx, kv8, scale, scale_block: int, ws, stream=None):
+    _check("dsa_project_append_q8", lib().dsa_project_append_q8(
+        ctypes.byref(batch.struct), _ptr(hidden), _ptr(w_all), d_model, H_I, H, rope_base, _ptr(q_idx), _ptr(w),
+        _ptr(q), _ptr(k_idx), _ptr(kv8), _ptr(scale), scale_block, _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def dsa_sparse_mla_q8(batch: DeviceBatch, q, kv8, scale, scale_block: int, idx, k: int, H: int, sm_scale: float, out,
+                      lse, ws, stream=None):
+    """Attention over the 8-bit cache; idx = None with k = 0 attends to every visible key."""
+    _check("dsa_sparse_mla_q8", lib().dsa_sparse_mla_q8(
+        ctypes.byref(batch.struct), _ptr(q), _ptr(kv8), _ptr(scale), scale_block, _ptr(idx), k, H, sm_scale,
+        _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def dsa_forward_q8(batch: DeviceBatch, q_idx, k_idx, w, H_I: int, q, kv8, scale, scale_block: int, H: int, k: int,
+                   sm_scale: float, out, lse, ws, stream=None):
+    _check("dsa_forward_q8", lib().dsa_forward_q8(
+        ctypes.byref(batch.struct), _ptr(q_idx), _ptr(k_idx), _ptr(w), H_I, _ptr(q), _ptr(kv8), _ptr(scale),
+        scale_block, H, k, sm_scale, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def _buffers(buffers: PageBuffers | None):
+    return ctypes.byref(buffers.struct) if buffers is not None else None
+
+
+def _entries(fn: str, a: torch.Tensor, b: torch.Tensor) -> int:
+    if a.dtype != torch.int32 or b.dtype != torch.int32 or a.numel() != b.numel():
+        raise ValueError(f"{fn} takes two int32 lists of one length")
+    return a.numel()
+
+
+def dsa_pages_resize(src: PageState, dst: PageState, seqs, new_len, buffers: PageBuffers | None, ws, stream=None):
+    """Sets sequence lengths: src -> dst (the same state: in place)."""
+    n = _entries("dsa_pages_resize", seqs, new_len)
+    _check("dsa_pages_resize", lib().dsa_pages_resize(
+        ctypes.byref(src.struct), ctypes.byref(dst.struct), n, _ptr(seqs), _ptr(new_len), _buffers(buffers),
+        _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def dsa_pages_fork(src: PageState, dst: PageState, src_seqs, dst_seqs, ws, stream=None):
+    n = _entries("dsa_pages_fork", src_seqs, dst_seqs)
+    _check("dsa_pages_fork", lib().dsa_pages_fork(
+        ctypes.byref(src.struct), ctypes.byref(dst.struct), n, _ptr(src_seqs), _ptr(dst_seqs), _ptr(ws), ws.numel(),
+        _stream(stream)))
+
+
+def dsa_pages_compact(src: PageState, dst: PageState, buffers: PageBuffers | None, page_map, ws, stream=None):
+    """Moves the pages in use to the front of the pool; page_map (int32 [num_pages] or
+    None) receives the new place of each page that was in use."""
+    _check("dsa_pages_compact", lib().dsa_pages_compact(
+        ctypes.byref(src.struct), ctypes.byref(dst.struct), _buffers(buffers), _ptr(page_map), _ptr(ws), ws.numel(),
+        _stream(stream)))
 
 
 def forward_ws_views(batch: DeviceBatch, H_I: int, H: int, k: int, ws) -> tuple[int, int, int]:

@@ -135,6 +135,7 @@ struct ProjLayout {
   uint32_t* status;
   float* y;
   void* gemm_ws;
+  uint16_t* kv_new;          // bf16 [T, 576] (8-bit cache only)
   size_t bytes;
 };
 
@@ -148,6 +149,14 @@ ProjLayout proj_layout(void* ws, const dsa_batch* b, int H_I, int H) {
   L.gemm_ws = p + off;
   off += project_gemm_workspace_bytes();
   L.bytes = off;
+  return L;
+}
+
+// The projection's workspace plus the latent rows on their way to the 8-bit cache.
+ProjLayout proj_q8_layout(void* ws, const dsa_batch* b, int H_I, int H) {
+  ProjLayout L = proj_layout(ws, b, H_I, H);
+  L.kv_new = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + L.bytes);
+  L.bytes += align_up(static_cast<size_t>(b->num_q) * DSA_D_QK * sizeof(uint16_t));
   return L;
 }
 
@@ -335,6 +344,118 @@ dsa_status run_mla(const dsa_batch* b, const uint16_t* q, const uint16_t* kv, co
   return cuda_status(launch_sparse_mla(p, tq, st));
 }
 
+dsa_status run_project(const dsa_batch* batch, const uint16_t* hidden, const uint16_t* w_all, int d_model, int H_I,
+                       int H, float rope_base, uint8_t* q_idx, float* w, uint16_t* q, uint8_t* k_idx, uint16_t* kv,
+                       const ProjLayout& L, cudaStream_t st) {
+  if (batch->num_q == 0) return DSA_OK;
+  ProjParams p{};
+  p.y = L.y;
+  p.q_idx = q_idx;
+  p.w = w;
+  p.q = q;
+  p.k_cache = k_idx;
+  p.kv_cache = kv;
+  p.kv_new = L.kv_new;
+  p.q_seq = batch->q_seq;
+  p.q_pos = batch->q_pos;
+  p.kv_offset = batch->kv_offset;
+  p.kv_len = batch->kv_len;
+  p.page_table = batch->page_table;
+  p.page_size = batch->page_size;
+  p.pages_per_seq = batch->pages_per_seq;
+  p.num_seqs = batch->num_seqs;
+  p.kv_rows = batch->kv_rows;
+  p.T = batch->num_q;
+  p.n_all = proj_rows(H_I, H);
+  p.hi = H_I;
+  p.heads = H;
+  p.rope_base = rope_base;
+  p.status = L.status;
+  bool gemm_failed = false;
+  const cudaError_t e = launch_project(p, hidden, w_all, d_model, L.gemm_ws, project_gemm_workspace_bytes(), st,
+                                       &gemm_failed);
+  return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- the 8-bit latent cache
+bool block_ok(int g) { return g >= 1 && g <= 64 && (g & (g - 1)) == 0; }
+bool k_q8_ok(const int32_t* idx, int k) { return idx ? k_ok(k) : k == 0; }
+bool finite(float x) { return x - x == 0.f; }
+
+struct Q8Layout {
+  uint32_t* status;
+  WsLayout fwd;              // plan, scores and idx of the forward
+  size_t bytes;
+};
+
+Q8Layout q8_layout(void* ws, int op, const dsa_batch* b, int H, int k) {
+  Q8Layout L{};
+  (void)H;
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  size_t off = kWsHeader;
+  L.status = reinterpret_cast<uint32_t*>(p);
+  if (op == DSA_Q8_FORWARD) {
+    L.fwd.status = L.status;
+    L.fwd.plan = reinterpret_cast<int32_t*>(p + off);
+    off += plan_bytes(b);
+    L.fwd.scores = reinterpret_cast<float*>(p + off);
+    off += align_up(static_cast<size_t>(b->num_q) * default_ld(b) * sizeof(float));
+    L.fwd.idx = reinterpret_cast<int32_t*>(p + off);
+    off += align_up(static_cast<size_t>(b->num_q) * k * sizeof(int32_t));
+  }
+  L.bytes = off;
+  return L;
+}
+
+dsa_status run_quantize(const dsa_batch* b, const uint16_t* kv, uint8_t* kv8, float* scale, int block,
+                        uint32_t* status, cudaStream_t st) {
+  QuantParams p{};
+  p.kv = kv;
+  p.kv8 = kv8;
+  p.scale = scale;
+  p.block = block;
+  p.q_seq = b->q_seq;
+  p.q_pos = b->q_pos;
+  p.kv_offset = b->kv_offset;
+  p.kv_len = b->kv_len;
+  p.page_table = b->page_table;
+  p.page_size = b->page_size;
+  p.pages_per_seq = b->pages_per_seq;
+  p.num_seqs = b->num_seqs;
+  p.kv_rows = b->kv_rows;
+  p.T = b->num_q;
+  p.status = status;
+  return cuda_status(launch_quantize_append(p, st));
+}
+
+dsa_status run_mla_q8(const dsa_batch* b, const uint16_t* q, const uint8_t* kv8, const float* scale, int block,
+                      const int32_t* idx, int k, int H, float sm_scale, uint16_t* out, float* lse, const Q8Layout& L,
+                      cudaStream_t st) {
+  MlaQ8Params p{};
+  p.q = q;
+  p.kv8 = kv8;
+  p.scale = scale;
+  while ((1 << p.block_log2) < block) ++p.block_log2;
+  p.idx = idx;
+  p.k = k;
+  p.H = H;
+  p.sm_scale = sm_scale;
+  p.out = out;
+  p.lse = lse;
+  p.q_seq = b->q_seq;
+  p.q_pos = b->q_pos;
+  p.kv_offset = b->kv_offset;
+  p.kv_len = b->kv_len;
+  p.page_table = b->page_table;
+  p.page_size = b->page_size;
+  p.pages_per_seq = b->pages_per_seq;
+  p.num_seqs = b->num_seqs;
+  p.kv_rows = b->kv_rows;
+  p.T = b->num_q;
+  p.status = L.status;
+  return cuda_status(launch_sparse_mla_q8(p, st));
+}
+
 }  // namespace
 }  // namespace dsa
 
@@ -515,33 +636,7 @@ dsa_status dsa_project_append(const dsa_batch* batch, const uint16_t* hidden, co
   if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(L.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
-  if (batch->num_q == 0) return DSA_OK;
-  ProjParams p{};
-  p.y = L.y;
-  p.q_idx = q_idx;
-  p.w = w;
-  p.q = q;
-  p.k_cache = k_idx;
-  p.kv_cache = kv;
-  p.q_seq = batch->q_seq;
-  p.q_pos = batch->q_pos;
-  p.kv_offset = batch->kv_offset;
-  p.kv_len = batch->kv_len;
-  p.page_table = batch->page_table;
-  p.page_size = batch->page_size;
-  p.pages_per_seq = batch->pages_per_seq;
-  p.num_seqs = batch->num_seqs;
-  p.kv_rows = batch->kv_rows;
-  p.T = batch->num_q;
-  p.n_all = proj_rows(H_I, H);
-  p.hi = H_I;
-  p.heads = H;
-  p.rope_base = rope_base;
-  p.status = L.status;
-  bool gemm_failed = false;
-  const cudaError_t e = launch_project(p, hidden, w_all, d_model, L.gemm_ws, project_gemm_workspace_bytes(), st,
-                                       &gemm_failed);
-  return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return run_project(batch, hidden, w_all, d_model, H_I, H, rope_base, q_idx, w, q, k_idx, kv, L, st);
 }
 
 dsa_status dsa_forward_host(const dsa_batch* batch, const uint8_t* h_q_idx, const float* h_w, const uint16_t* h_q,
@@ -602,6 +697,88 @@ dsa_status dsa_forward_host(const dsa_batch* batch, const uint8_t* h_q_idx, cons
       return DSA_ERR_CUDA;
   }
   return order_after(E, s_out, s_cp) ? DSA_OK : DSA_ERR_CUDA;
+}
+
+size_t dsa_q8_workspace_size(int op, const dsa_batch* batch, int H_I, int H, int k) {
+  if (!batch_ok(batch) || op < DSA_Q8_APPEND || op > DSA_Q8_PROJECT) return 0;
+  if ((op == DSA_Q8_FORWARD || op == DSA_Q8_PROJECT) && !hi_ok(H_I)) return 0;
+  if (op != DSA_Q8_APPEND && !h_ok(H)) return 0;
+  if (op == DSA_Q8_FORWARD && !k_ok(k)) return 0;
+  if (op == DSA_Q8_MLA && k != 0 && !k_ok(k)) return 0;
+  if (op == DSA_Q8_PROJECT) return proj_q8_layout(nullptr, batch, H_I, H).bytes;
+  return q8_layout(nullptr, op, batch, H, k).bytes;
+}
+
+dsa_status dsa_quantize_append(const dsa_batch* batch, const uint16_t* kv, uint8_t* kv8, float* scale, int scale_block,
+                               void* ws, size_t ws_bytes, void* stream) {
+  if (!batch_ok(batch) || !ws) return DSA_ERR_INVALID_ARGUMENT;
+  if (batch->num_q > 0 && (!kv || !kv8 || !scale)) return DSA_ERR_INVALID_ARGUMENT;
+  if (!block_ok(scale_block) || !paging_ok(batch)) return DSA_ERR_UNSUPPORTED;
+  if (!aligned16(kv) || !aligned16(kv8) || !aligned16(ws)) return DSA_ERR_UNSUPPORTED;
+  const Q8Layout L = q8_layout(ws, DSA_Q8_APPEND, batch, 8, 0);
+  if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(L.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
+  return run_quantize(batch, kv, kv8, scale, scale_block, L.status, st);
+}
+
+dsa_status dsa_project_append_q8(const dsa_batch* batch, const uint16_t* hidden, const uint16_t* w_all, int d_model,
+                                 int H_I, int H, float rope_base, uint8_t* q_idx, float* w, uint16_t* q,
+                                 uint8_t* k_idx, uint8_t* kv8, float* scale, int scale_block, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  if (!batch_ok(batch) || !ws) return DSA_ERR_INVALID_ARGUMENT;
+  if (batch->num_q > 0 && (!hidden || !w_all || !q_idx || !w || !q || !k_idx || !kv8 || !scale))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (d_model <= 0 || !(rope_base > 0.f)) return DSA_ERR_INVALID_ARGUMENT;
+  if (!hi_ok(H_I) || !h_ok(H) || d_model % 8 != 0 || !block_ok(scale_block) || !paging_ok(batch))
+    return DSA_ERR_UNSUPPORTED;
+  if (!aligned16(hidden) || !aligned16(w_all) || !aligned16(q_idx) || !aligned16(w) || !aligned16(q) ||
+      !aligned16(k_idx) || !aligned16(kv8) || !aligned16(ws))
+    return DSA_ERR_UNSUPPORTED;
+  const ProjLayout L = proj_q8_layout(ws, batch, H_I, H);
+  if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(L.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
+  const dsa_status s = run_project(batch, hidden, w_all, d_model, H_I, H, rope_base, q_idx, w, q, k_idx, nullptr, L, st);
+  if (s != DSA_OK) return s;
+  return run_quantize(batch, L.kv_new, kv8, scale, scale_block, L.status, st);
+}
+
+dsa_status dsa_sparse_mla_q8(const dsa_batch* batch, const uint16_t* q, const uint8_t* kv8, const float* scale,
+                             int scale_block, const int32_t* idx, int k, int H, float sm_scale, uint16_t* out,
+                             float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!batch_ok(batch) || !ws) return DSA_ERR_INVALID_ARGUMENT;
+  if (batch->num_q > 0 && (!q || !kv8 || !scale || !out)) return DSA_ERR_INVALID_ARGUMENT;
+  if (!finite(sm_scale)) return DSA_ERR_INVALID_ARGUMENT;
+  if (!h_ok(H) || !k_q8_ok(idx, k) || !block_ok(scale_block) || !paging_ok(batch)) return DSA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(kv8) || !aligned16(out) || !aligned16(ws)) return DSA_ERR_UNSUPPORTED;
+  const Q8Layout L = q8_layout(ws, DSA_Q8_MLA, batch, H, k);
+  if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(L.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
+  return run_mla_q8(batch, q, kv8, scale, scale_block, idx, k, H, sm_scale, out, lse, L, st);
+}
+
+dsa_status dsa_forward_q8(const dsa_batch* batch, const uint8_t* q_idx, const uint8_t* k_idx, const float* w, int H_I,
+                          const uint16_t* q, const uint8_t* kv8, const float* scale, int scale_block, int H, int k,
+                          float sm_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!batch_ok(batch) || !ws) return DSA_ERR_INVALID_ARGUMENT;
+  if (batch->num_q > 0 && (!q_idx || !k_idx || !w || !q || !kv8 || !scale || !out)) return DSA_ERR_INVALID_ARGUMENT;
+  if (!finite(sm_scale)) return DSA_ERR_INVALID_ARGUMENT;
+  if (!hi_ok(H_I) || !h_ok(H) || !k_ok(k) || !block_ok(scale_block) || !paging_ok(batch)) return DSA_ERR_UNSUPPORTED;
+  if (!aligned16(q_idx) || !aligned16(k_idx) || !aligned16(w) || !aligned16(q) || !aligned16(kv8) ||
+      !aligned16(out) || !aligned16(ws))
+    return DSA_ERR_UNSUPPORTED;
+  const Q8Layout L = q8_layout(ws, DSA_Q8_FORWARD, batch, H, k);
+  if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(L.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
+  const int64_t ld = default_ld(batch);
+  dsa_status s = run_indexer(batch, q_idx, k_idx, w, H_I, L.fwd.scores, ld, L.fwd, st);
+  if (s != DSA_OK) return s;
+  s = run_topk(batch, L.fwd.scores, ld, k, L.fwd.idx, L.fwd, st);
+  if (s != DSA_OK) return s;
+  return run_mla_q8(batch, q, kv8, scale, scale_block, L.fwd.idx, k, H, sm_scale, out, lse, L, st);
 }
 
 dsa_status dsa_forward_ws_views(const dsa_batch* batch, int H_I, int H, int k, void* ws, float** scores, int64_t* ld,

@@ -82,7 +82,8 @@ struct ProjParams {
   float* w;                  // [T, H_I]
   uint16_t* q;               // [T, H, 576] bf16
   uint8_t* k_cache;          // [kv_rows, 128] E4M3
-  uint16_t* kv_cache;        // [kv_rows, 576] bf16
+  uint16_t* kv_cache;        // [kv_rows, 576] bf16, or null with kv_new
+  uint16_t* kv_new;          // [T, 576] bf16: latent rows by token instead of by cache row, or null
   const int32_t* q_seq;
   const int32_t* q_pos;
   const int64_t* kv_offset;  // contiguous layout
@@ -124,6 +125,84 @@ struct MlaBwdParams {
   uint32_t* status;
 };
 cudaError_t launch_mla_backward(const MlaBwdParams& p, cudaStream_t stream);
+
+struct QuantParams {
+  const uint16_t* kv;        // [T, 576] bf16, the new rows
+  uint8_t* kv8;              // [kv_rows, 576] E4M3
+  float* scale;              // [ceil(kv_rows / block)]
+  int block;                 // tokens per scale
+  const int32_t* q_seq;
+  const int32_t* q_pos;
+  const int64_t* kv_offset;  // contiguous layout
+  const int32_t* kv_len;
+  const int32_t* page_table; // paged layout (page_size > 0)
+  int page_size;
+  int pages_per_seq;
+  int num_seqs;
+  int64_t kv_rows;
+  int T;
+  int window;                // tokens that a CTA looks at
+  uint32_t* status;
+};
+cudaError_t launch_quantize_append(const QuantParams& p, cudaStream_t stream);
+
+struct MlaQ8Params {
+  const uint16_t* q;         // [T, H, 576] bf16
+  const uint8_t* kv8;        // [kv_rows, 576] E4M3
+  const float* scale;        // [ceil(kv_rows / block)]
+  int block_log2;            // tokens per scale = 1 << block_log2
+  const int32_t* idx;        // [T, k], or null: every visible key
+  int k;
+  int H;
+  float sm_scale;
+  uint16_t* out;             // [T, H, 512] bf16
+  float* lse;                // [T, H] or null
+  const int32_t* q_seq;
+  const int32_t* q_pos;
+  const int64_t* kv_offset;  // contiguous layout
+  const int32_t* kv_len;
+  const int32_t* page_table; // paged layout (page_size > 0)
+  int page_size;
+  int pages_per_seq;
+  int num_seqs;
+  int64_t kv_rows;
+  int T;
+  uint32_t* status;
+};
+cudaError_t launch_sparse_mla_q8(const MlaQ8Params& p, cudaStream_t stream);
+
+struct PagesParams {
+  int num_seqs, num_pages, page_size, pages_per_seq;
+  const int32_t* table_in;   // [num_seqs, pages_per_seq]
+  const int32_t* len_in;     // [num_seqs]
+  const int32_t* ref_in;     // [num_pages]
+  int32_t* table_out;        // the same arrays, or others
+  int32_t* len_out;
+  int32_t* ref_out;
+  int n;                     // entries of the lists
+  const int32_t* list_a;     // sequences (resize), sources (fork)
+  const int32_t* list_b;     // new lengths (resize), destinations (fork)
+  uint8_t* buf[DSA_MAX_PAGE_BUFFERS];
+  int64_t buf_bytes[DSA_MAX_PAGE_BUFFERS];
+  int buf_chunks[DSA_MAX_PAGE_BUFFERS];
+  int buf_vec[DSA_MAX_PAGE_BUFFERS];
+  int num_bufs;
+  int chunks;                // of one page, over all buffers
+  // workspace
+  uint32_t* status;
+  int32_t* num_moves;        // [1]
+  int32_t* first;            // [num_seqs]
+  int32_t* sharers;          // [num_pages]
+  int32_t* last_sharer;      // [num_pages]
+  int32_t* free_list;        // [num_pages]
+  int32_t* map;              // [num_pages]
+  int32_t* move_src;         // [num_pages]
+  int32_t* move_dst;         // [num_pages]
+  int32_t* old_len;          // [n]
+  int32_t* entry_ok;         // [n]
+  int32_t* start;            // [n]
+  int32_t* copies;           // [n]
+};
 
 // Counts kernel launches made by the library (dsa_launch_count).
 void count_launches(int n);

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kProjThreads) project_epilogue_kernel(ProjPara
   for (int j = tid; j < HI; j += kProjThreads) p.w[static_cast<int64_t>(t) * HI + j] = y[o_w + j];
   // latent row [latent 512, rotated RoPE key 64] -> bf16 cache row (4 values per step)
   if (row >= 0) {
-    uint16_t* kvr = p.kv_cache + row * DSA_D_QK;
+    uint16_t* kvr = p.kv_new ? p.kv_new + static_cast<int64_t>(t) * DSA_D_QK : p.kv_cache + row * DSA_D_QK;
     for (int j = tid; j < DSA_D_QK / 4; j += kProjThreads) {
       const float4 v = *reinterpret_cast<const float4*>(y + o_lat + j * 4);   // o_kr = o_lat + 512
       float a0 = v.x, b0 = v.y, a1 = v.z, b1 = v.w;
