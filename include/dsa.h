@@ -431,10 +431,10 @@ dsa_status dsa_project_append_q8(const dsa_batch *batch, const uint16_t *hidden,
  *       form, every visible key 0 .. q_pos[t] of any context length
  * The cache's codes are the tensor cores' operand as they are; the bf16 queries and
  * the softmax weights (times their rows' scales) enter as sums of two E4M3 numbers,
- * which hold 8 significant bits like bf16.  Per query and head the weights are held
- * relative to the largest p_i * scale_i, to 2^-18 of it absolutely, and the
- * query's entries relative to its largest one, to 2^-18.  fp32 logits, softmax
- * statistics and sums.  A query row with an infinite or NaN entry gives NaN, and so
+ * which hold 8 significant bits like bf16, down to an absolute error of 2^-15 of the
+ * largest p_i * scale_i of the query and head (weights) and of 2^-17 of the
+ * largest entry of the query's head (queries).  fp32 logits, softmax statistics
+ * and sums.  A query row with an infinite or NaN entry gives NaN, and so
  * does a selected row with a NaN code.
  * A row whose scale is outside [2^-100, 2^100] raises DSA_DEV_BAD_SCALE and is
  * skipped.  In the dense form a query position outside its sequence raises

@@ -381,19 +381,32 @@ dsa_status run_project(const dsa_batch* batch, const uint16_t* hidden, const uin
 bool block_ok(int g) { return g >= 1 && g <= 64 && (g & (g - 1)) == 0; }
 bool k_q8_ok(const int32_t* idx, int k) { return idx ? k_ok(k) : k == 0; }
 bool finite(float x) { return x - x == 0.f; }
+bool rows_q8_ok(const dsa_batch* b) { return b->kv_rows < (int64_t{1} << 31); }   // the kernels keep rows in 32 bits
 
 struct Q8Layout {
   uint32_t* status;
   WsLayout fwd;              // plan, scores and idx of the forward
+  int splits, split_tiles;   // of the attention
+  float* part_o;
+  float* part_lse;
   size_t bytes;
 };
 
 Q8Layout q8_layout(void* ws, int op, const dsa_batch* b, int H, int k) {
   Q8Layout L{};
-  (void)H;
   uint8_t* p = static_cast<uint8_t*>(ws);
   size_t off = kWsHeader;
   L.status = reinterpret_cast<uint32_t*>(p);
+  if (op == DSA_Q8_MLA || op == DSA_Q8_FORWARD) {
+    L.splits = mla_q8_plan(b->num_q, H, k > 0 ? k : b->max_kv_len, num_sms(), &L.split_tiles);
+    if (L.splits > 1) {
+      const size_t rows = static_cast<size_t>(b->num_q) * L.splits * H;
+      L.part_o = reinterpret_cast<float*>(p + off);
+      off += align_up(rows * DSA_D_V * sizeof(float));
+      L.part_lse = reinterpret_cast<float*>(p + off);
+      off += align_up(rows * sizeof(float));
+    }
+  }
   if (op == DSA_Q8_FORWARD) {
     L.fwd.status = L.status;
     L.fwd.plan = reinterpret_cast<int32_t*>(p + off);
@@ -453,7 +466,11 @@ dsa_status run_mla_q8(const dsa_batch* b, const uint16_t* q, const uint8_t* kv8,
   p.kv_rows = b->kv_rows;
   p.T = b->num_q;
   p.status = L.status;
-  return cuda_status(launch_sparse_mla_q8(p, st));
+  p.splits = L.splits;
+  p.split_tiles = L.split_tiles;
+  p.part_o = L.part_o;
+  p.part_lse = L.part_lse;
+  return cuda_status(launch_sparse_mla_q8(p, num_sms(), st));
 }
 
 }  // namespace
@@ -750,7 +767,7 @@ dsa_status dsa_sparse_mla_q8(const dsa_batch* batch, const uint16_t* q, const ui
   if (!batch_ok(batch) || !ws) return DSA_ERR_INVALID_ARGUMENT;
   if (batch->num_q > 0 && (!q || !kv8 || !scale || !out)) return DSA_ERR_INVALID_ARGUMENT;
   if (!finite(sm_scale)) return DSA_ERR_INVALID_ARGUMENT;
-  if (!h_ok(H) || !k_q8_ok(idx, k) || !block_ok(scale_block) || !paging_ok(batch)) return DSA_ERR_UNSUPPORTED;
+  if (!h_ok(H) || !k_q8_ok(idx, k) || !block_ok(scale_block) || !paging_ok(batch) || !rows_q8_ok(batch)) return DSA_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(kv8) || !aligned16(out) || !aligned16(ws)) return DSA_ERR_UNSUPPORTED;
   const Q8Layout L = q8_layout(ws, DSA_Q8_MLA, batch, H, k);
   if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
@@ -765,7 +782,8 @@ dsa_status dsa_forward_q8(const dsa_batch* batch, const uint8_t* q_idx, const ui
   if (!batch_ok(batch) || !ws) return DSA_ERR_INVALID_ARGUMENT;
   if (batch->num_q > 0 && (!q_idx || !k_idx || !w || !q || !kv8 || !scale || !out)) return DSA_ERR_INVALID_ARGUMENT;
   if (!finite(sm_scale)) return DSA_ERR_INVALID_ARGUMENT;
-  if (!hi_ok(H_I) || !h_ok(H) || !k_ok(k) || !block_ok(scale_block) || !paging_ok(batch)) return DSA_ERR_UNSUPPORTED;
+  if (!hi_ok(H_I) || !h_ok(H) || !k_ok(k) || !block_ok(scale_block) || !paging_ok(batch) || !rows_q8_ok(batch))
+    return DSA_ERR_UNSUPPORTED;
   if (!aligned16(q_idx) || !aligned16(k_idx) || !aligned16(w) || !aligned16(q) || !aligned16(kv8) ||
       !aligned16(out) || !aligned16(ws))
     return DSA_ERR_UNSUPPORTED;

@@ -168,8 +168,16 @@ struct MlaQ8Params {
   int64_t kv_rows;
   int T;
   uint32_t* status;
+  int splits;                // parts of each query's row list (1 = no combine pass)
+  int split_tiles;           // 128-row tiles of a part
+  int groups;                // head groups
+  int items;                 // T * splits * groups
+  float* part_o;             // [T, splits, H, 512] fp32 (splits > 1)
+  float* part_lse;           // [T, splits, H]       fp32 (splits > 1)
 };
-cudaError_t launch_sparse_mla_q8(const MlaQ8Params& p, cudaStream_t stream);
+// Parts that each query's row list is cut into, and the 128-row tiles of a part.
+int mla_q8_plan(int T, int H, int max_entries, int sms, int* split_tiles);
+cudaError_t launch_sparse_mla_q8(const MlaQ8Params& p, int sms, cudaStream_t stream);
 
 struct PagesParams {
   int num_seqs, num_pages, page_size, pages_per_seq;
