@@ -22,11 +22,12 @@
 // One CTA per SM works through items (query, 64 heads, split of the row list).
 // TMEM (512 columns): two S^T buffers of 128 columns, O^T as 4 x 64 columns.
 // Shared memory (227 KB): Q 72 KB, two row tiles of 72 KB, W_lo 8 KB; W_hi lies over
-// the row tile's RoPE part, which only the first product reads.  W_lo has one
-// buffer, so the second product takes it first and gives it back half way.
-// 20 warps: 0-3 and 4-7 softmax and output (one thread per row, 32 heads each), 8-15
-// row gathers (16-byte cp.async) and the queries' hi/lo split, 16 issues S^T, 17 O^T.
-// Registers: launched at 96 per thread, softmax 128, gathers 80, issuers 64.
+// the row tile's RoPE part, which only the first product reads.  The second product
+// goes by quarters of 32 rows (one K step, all dims, lo and hi), each of which gives
+// its rows and weights back, so the next tile's rows and weights follow it closely.
+// 28 warps: 0-15 softmax, output and the next queries' hi/lo split (warp w: rows
+// 32 (w mod 4) .., 16 heads), 16-23 row gathers (16-byte cp.async), 24 issues S^T, 25
+// O^T.  Registers: launched at 72 per thread, softmax 88, gathers 56, issuers 40.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -40,18 +41,18 @@ namespace {
 
 constexpr int kHT = 64;                            // heads per CTA
 constexpr int kRows = 128;                         // rows per tile
-constexpr int kSoftWarps = 8;
+constexpr int kSoftWarps = 16;
+constexpr int kGroups = kSoftWarps / 4;            // softmax groups of four warps (128 rows)
+constexpr int kGH = kHT / kGroups;                 // heads per group
 constexpr int kGatherWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + kGatherWarps + 4);
-constexpr int kLaunchRegs = 96, kSoftRegs = 128, kGatherRegs = 80, kIssueRegs = 64;
+constexpr int kLaunchRegs = 72, kSoftRegs = 88, kGatherRegs = 56, kIssueRegs = 40;
 static_assert(32 * (kSoftWarps * kSoftRegs + kGatherWarps * kGatherRegs + 4 * kIssueRegs) == kThreads * kLaunchRegs,
               "the register split must add up to the launch allocation");
 constexpr uint32_t kSCol = 0, kOCol = 256;         // TMEM columns
 constexpr float kTop = 5.f;                        // log2 of the largest weight when m is set
 constexpr float kLimit = 8.5f;                     // log2 of the weight that makes m move
 constexpr int kMaxSplits = 64;
-constexpr int kBarSoft = 1;                        // named barriers: 1, 2 softmax groups, 3 gathers
-constexpr int kBarGather = 3;
 
 struct Tile {                                      // 128 rows: latent as 4 x 128 B (SW128), RoPE 64 B (SW64)
   uint8_t lat[4][kRows * 128];
@@ -63,11 +64,12 @@ struct Q8Smem {
   Tile rows[2];
   uint8_t w_lo[kRows * 64];
   float s_row[2][kRows];                           // row scales, 0 = unused row
-  float red[2][4][32];
-  float qs[2][kHT];                                // 2^-e of each head's query
+  float red[kGroups][4][kGH];
+  uint16_t qs[2][kHT];                             // 2^-e of each head's query, bf16
   float m[kHT];
-  uint64_t rows_full[2], rows_empty[2], s_full[2], s_free[2], w_full, wlo_free, q_full, q_free, o_full, o_free,
-      plan_full[2], plan_free[2], done;
+  uint64_t rows_full[2], rows_empty[2][4], s_full[2], s_free[2], w_full[4], q_full, q_free, o_full, o_free,
+      plan_full[2], plan_free[2], vote[kGroups], sync[kGroups], gather_sync, done;
+  int over[kGroups][2];                            // a weight of the group passed the limit (by tile parity)
   int plan[2];                                     // tiles of the item
   int last[kGatherWarps];
   uint32_t tmem;
@@ -91,17 +93,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t threads, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
-      : "memory");
-  return r != 0;
-}
-
 // Two fp32 -> E4M3 hi and lo with hi + lo = the value to 8 significant bits (low byte
 // = a).  Through fp16, which holds 11 bits: |x| <= 448 and steps of 2^-24 near zero,
 // both beyond what hi and lo can hold.
@@ -118,11 +109,20 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 }
 
 // Bounded wait that gives up at once when a thread of the CTA has given up.  Warps
-// that meet on a named barrier leave their loops together: they agree on it there
-// (bar_or), so none is left waiting.
+// meet on such waits only (no named barriers), so one that leaves strands no other.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* ab) {
   if (mbar_try_wait(smem_u32(bar), parity)) return true;
   return *ab == 0 && mbar_wait(bar, parity, status, ab);
+}
+
+// The warps of a group meet (`bar` counts one arrival per warp, `phase` its use).
+__device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& phase, int lane, uint32_t* status, volatile int* ab) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+  const bool ok = wait(bar, phase & 1, status, ab);
+  ++phase;
+  __syncwarp();
+  return ok;
 }
 
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -131,11 +131,11 @@ __device__ __forceinline__ float lg2_approx(float x) {
   return y;
 }
 
-// v[0] of lane l = the reduction of v[l] over the warp's lanes.
+// The reduction of v[l mod 16] over the warp's lanes, for lane l.
 template <bool kMax>
-__device__ __forceinline__ float reduce_transposed(float (&v)[32], int lane) {
+__device__ __forceinline__ float reduce_transposed(float (&v)[16], int lane) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = 8; o > 0; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -144,7 +144,8 @@ __device__ __forceinline__ float reduce_transposed(float (&v)[32], int lane) {
       v[i] = kMax ? fmaxf(keep, got) : keep + got;
     }
   }
-  return v[0];
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
+  return kMax ? fmaxf(v[0], got) : v[0] + got;
 }
 
 // An item: query t, heads 64 hg .., entries [e0, e1) of its row list.
@@ -181,6 +182,57 @@ __device__ __forceinline__ void item_list(const MlaQ8Params& p, Item& I) {
   I.e1 = I.ok ? min(n, I.e0 + p.split_tiles * kRows) : I.e0;
 }
 
+// Splits the 64 heads' queries of an item into hi and lo (this warp: heads warp + 16 i)
+// and stores them as the first product's operand.
+__device__ __forceinline__ void split_queries(const MlaQ8Params& p, Q8Smem& S, int t, int hg, uint32_t slot, int warp,
+                                              int lane) {
+#pragma unroll 1
+  for (int i0 = 0; i0 < kHT / kSoftWarps; i0 += 2) {
+    uint32_t w[2][9];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int h = hg * kHT + warp + (i0 + u) * kSoftWarps;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (static_cast<int64_t>(t) * p.H + h) * DSA_D_QK);
+#pragma unroll
+      for (int i = 0; i < 9; ++i) w[u][i] = h < p.H ? __ldg(src + i * 32 + lane) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int hl = warp + (i0 + u) * kSoftWarps;
+      uint32_t am = 0;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) am = max(am, max(w[u][i] & 0x7fffu, (w[u][i] >> 16) & 0x7fffu));
+      am = __reduce_max_sync(0xffffffffu, am);
+      // times 2^e: the largest entry in [2^7, 2^8)
+      int e = am >= 0x80u ? 7 + 127 - static_cast<int>(am >> 7) : 120;
+      e = e > 120 ? 120 : (e < -120 ? -120 : e);
+      const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+      if (lane == 0) S.qs[slot][hl] = static_cast<uint16_t>((127 - e) << 7);
+      const bool bad = am >= 0x7f80u;               // an infinity or NaN: the head's results are NaN
+      uint8_t* lat = &S.q.lat[0][hl * 128];
+      const uint32_t col = 2 * lane & 63;           // bytes 64 i + 2 lane of the row
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        uint32_t hi, lo;
+        split2(__uint_as_float(w[u][i] << 16) * up, __uint_as_float(w[u][i] & 0xffff0000u) * up, hi, lo);
+        if (bad) hi = 0x7f7fu;
+        if (i < 8) {
+          const uint32_t at = (((col >> 4) + (i & 1) * 4) ^ (hl & 7)) * 16 + (col & 15) + (i >> 1) * (kRows * 128);
+          *reinterpret_cast<uint16_t*>(lat + at) = static_cast<uint16_t>(hi);
+          *reinterpret_cast<uint16_t*>(lat + at + kHT * 128) = static_cast<uint16_t>(lo);
+        } else {
+          const uint32_t at = hl * 64 + ((col >> 4) ^ ((hl >> 1) & 3)) * 16 + (col & 15);
+          *reinterpret_cast<uint16_t*>(&S.q.rope[at]) = static_cast<uint16_t>(hi);
+          *reinterpret_cast<uint16_t*>(&S.q.rope[at + kHT * 64]) = static_cast<uint16_t>(lo);
+        }
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&S.q_full);
+}
+
 __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
   extern __shared__ __align__(1024) uint8_t raw[];
   Q8Smem& S = *reinterpret_cast<Q8Smem*>(raw);
@@ -194,21 +246,27 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&S.rows_full[b], 32 * kGatherWarps + kGatherWarps);
-      mbar_init(&S.rows_empty[b], 1);
       mbar_init(&S.s_full[b], 1);
       mbar_init(&S.s_free[b], kSoftWarps);
       mbar_init(&S.plan_full[b], 1);
       mbar_init(&S.plan_free[b], kSoftWarps + 2);
+      for (int k = 0; k < 4; ++k) mbar_init(&S.rows_empty[b][k], 1);
     }
-    mbar_init(&S.w_full, kSoftWarps);
-    mbar_init(&S.wlo_free, 1);
-    mbar_init(&S.q_full, kGatherWarps);
+    for (int k = 0; k < 4; ++k) mbar_init(&S.w_full[k], kGroups);
+    for (int k = 0; k < kGroups; ++k) {
+      mbar_init(&S.vote[k], 4);
+      mbar_init(&S.sync[k], 4);
+      S.over[k][0] = S.over[k][1] = 0;
+    }
+    mbar_init(&S.gather_sync, kGatherWarps);
+    mbar_init(&S.q_full, kSoftWarps);
     mbar_init(&S.q_free, 1);
     mbar_init(&S.o_full, 1);
     mbar_init(&S.o_free, kSoftWarps);
     mbar_init(&S.done, 2);
     fence_mbar_init();
   }
+  if (tid < kHT) S.m[tid] = 0.f;
   if (warp == kSoftWarps + kGatherWarps) tmem_alloc(&S.tmem, 512);
   tc_fence_before();
   __syncthreads();
@@ -217,181 +275,233 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
   const int step = gridDim.x;
 
   if (warp < kSoftWarps) {
-    // ================================================================ softmax and output
+    // ================================================================ softmax, output, queries
     setmaxnreg_inc<kSoftRegs>();
-    const int grp = warp >> 2, quad = warp & 3;     // heads 32 grp .., rows 32 quad ..
+    const int grp = warp >> 2, quad = warp & 3;     // heads 16 grp .., rows 32 quad ..
     const int r = quad * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t s_at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kSCol + grp * kGH;
+    const uint32_t o_at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kOCol + grp * kGH;
     const float c0 = p.sm_scale * 1.4426950408889634f;
-    uint32_t g = 0, items_done = 0;                 // tiles and non-empty items so far
-    bool bad = false;                               // a wait of this thread ran out
+    uint32_t g = 0, nq = 0, met = 0;                // tiles, non-empty items, meetings of the group so far
+    bool bad = false;                               // a wait ran out
+    int tiles = 0, tiles_next = 0, tiles_last = 0;  // of this item, the next, the last non-empty one
+    // the tiles of the kk-th item, and its queries' operand if it has any
+    auto next_queries = [&](int kk, int it) {
+      bad |= !wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
+      tiles_next = S.plan[kk & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
+      if (tiles_next == 0) return;
+      bad |= nq > 0 && !wait(&S.q_free, (nq - 1) & 1, p.status, ab);
+      // qs has two places: every warp must be through with the logits of the item before
+      // the last one (it is, unless the last one's only tile may have run ahead)
+      if (tiles_last == 1 && g > 1) bad |= !wait(&S.s_free[g & 1], ((g - 2) >> 1) & 1, p.status, ab);
+      __syncwarp();
+      Item I;
+      item_place(p, it, I);
+      split_queries(p, S, I.t, I.hg, nq & 1, warp, lane);
+    };
+    if (blockIdx.x < p.items) next_queries(0, blockIdx.x);
     for (int kk = 0, it = blockIdx.x; it < p.items; ++kk, it += step) {
       Item I;
       item_place(p, it, I);
-      bad |= !wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
-      const int tiles = S.plan[kk & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
-      const int h0 = I.hg * kHT + grp * 32;
-      const float* qs = S.qs[items_done & 1] + grp * 32;
-      float l[32];
+      tiles = tiles_next;
+      if (it + step < p.items) {                    // the next item's queries on their way to L2
+        Item N;
+        item_place(p, it + step, N);
+        const int h0 = N.hg * kHT, lines = min(kHT, p.H - h0) * 9;
+        const char* src = reinterpret_cast<const char*>(p.q + (static_cast<int64_t>(N.t) * p.H + h0) * DSA_D_QK);
+        for (int i = tid; i < lines; i += 32 * kSoftWarps)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i * 128));
+      }
+      const int h0 = I.hg * kHT + grp * kGH;
+      const uint32_t slot = nq & 1;
+      float l[kGH];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) l[i] = 0.f;
+      for (int i = 0; i < kGH; ++i) l[i] = 0.f;
       bool seen = false;                            // a usable row so far
-      if (quad == 0) S.m[grp * 32 + lane] = 0.f;
-      if (bar_or(kBarSoft + grp, 128, bad)) break;
-      bool stop = false;
+      if (tiles > 0) {
+        bad |= !wait(&S.q_full, nq & 1, p.status, ab);
+        ++nq;
+        tiles_last = tiles;
+      }
       for (int j = 0; j < tiles; ++j, ++g) {
         const int b = g & 1;
         const uint32_t ph = (g >> 1) & 1;
         bad |= !wait(&S.rows_full[b], ph, p.status, ab) || !wait(&S.s_full[b], ph, p.status, ab);
-        __syncwarp();
+        if ((bad = __any_sync(0xffffffffu, bad))) break;
         tc_fence_after();
         const float s = S.s_row[b][r];
         const float c = c0 * s;
         const float sg = s > 0.f ? lg2_approx(s) : -INFINITY;
         const float inv = s > 0.f ? 1.f / s : 0.f;
-        // x = b - m, the log2 of the weight
-        float x[32];
-        float top = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t hi[16], lo[16];
-          tmem_ld16(tmem + lanes + kSCol + b * 128 + grp * 32 + q * 16, hi);
-          tmem_ld16(tmem + lanes + kSCol + b * 128 + 64 + grp * 32 + q * 16, lo);
+        uint32_t wh[4], wl[4];
+        float ln[kGH];
+        // x = b - m, the log2 of the weight; the weights, split, and the denominators with them
+        float x[kGH];
+        auto logits = [&]() {
+          uint32_t hi[kGH], lo[kGH];
+          tmem_ld16(s_at + b * 128, hi);
+          tmem_ld16(s_at + b * 128 + kHT, lo);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const int h = q * 16 + i;
-            const float2 sc = *reinterpret_cast<const float2*>(&qs[h]);
-            const float2 mm = *reinterpret_cast<const float2*>(&S.m[grp * 32 + h]);
+          for (int i = 0; i < kGH; i += 2) {
+            const uint32_t sc = *reinterpret_cast<const uint32_t*>(&S.qs[slot][grp * kGH + i]);
+            const float2 mm = *reinterpret_cast<const float2*>(&S.m[grp * kGH + i]);
             const float2 d = make_float2(__uint_as_float(hi[i]) + __uint_as_float(lo[i]),
                                          __uint_as_float(hi[i + 1]) + __uint_as_float(lo[i + 1]));
-            const float2 y = ffma2(d, make_float2(sc.x * c, sc.y * c), make_float2(sg - mm.x, sg - mm.y));
-            x[h] = y.x;
-            x[h + 1] = y.y;
-            top = fmaxf(top, fmaxf(y.x, y.y));
+            const float2 y =
+                ffma2(d, make_float2(__uint_as_float(sc << 16) * c, __uint_as_float(sc & 0xffff0000u) * c),
+                      make_float2(sg - mm.x, sg - mm.y));
+            x[i] = y.x;
+            x[i + 1] = y.y;
           }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.s_free[b]);
-        const bool usable = s > 0.f;
-        if (bar_or(kBarSoft + grp, 128, bad || (seen ? top > kLimit : usable))) {
-          if ((stop = bar_or(kBarSoft + grp, 128, bad))) break;
-          // move the reference of the heads that need it (all of them at the first usable rows)
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = usable ? x[i] : -INFINITY;
-          S.red[grp][quad][lane] = reduce_transposed<true>(v, lane);
-          named_bar_sync(kBarSoft + grp, 128);
-          const float mx = fmaxf(fmaxf(S.red[grp][0][lane], S.red[grp][1][lane]),
-                                 fmaxf(S.red[grp][2][lane], S.red[grp][3][lane]));
-          const float up = (seen ? mx > kLimit : mx > -INFINITY) ? mx - kTop : 0.f;
-          const float f = ex2_approx(-up);          // of head 32 grp + lane
-          if (quad == 0) S.m[grp * 32 + lane] += up;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            x[i] -= __shfl_sync(0xffffffffu, up, i);
-            l[i] *= seen ? __shfl_sync(0xffffffffu, f, i) : 1.f;
-          }
-          if (seen) {
-            // O so far: wait for the product of the tile before this one
-            bad |= !wait(&S.rows_empty[b ^ 1], ((g - 1) >> 1) & 1, p.status, ab);
-            __syncwarp();
-            tc_fence_after();
-#pragma unroll 1
-            for (int q = 0; q < 8; ++q) {
-              const uint32_t at = tmem + lanes + kOCol + (q >> 1) * 64 + grp * 32 + (q & 1) * 16;
-              uint32_t o[16];
-              tmem_ld16(at, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xffffffffu, f, (q & 1) * 16 + i));
-              tmem_st16(at, o);
-            }
-            tmem_st_wait();
-          }
-          seen = true;
-          named_bar_sync(kBarSoft + grp, 128);      // m is set, red may be reused
-        }
-        // weights
-        bad |= g > 0 && !wait(&S.wlo_free, (g - 1) & 1, p.status, ab);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t wh[4], wl[4];
+        };
+        auto weights = [&]() {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t a0, b0, a1, b1;
             float w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = ex2_approx(x[q * 16 + i * 4 + e]);
+            for (int e = 0; e < 4; ++e) w[e] = ex2_approx(x[i * 4 + e]);
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-              const int h = q * 16 + i * 4 + e;
+              const int h = i * 4 + e;
               const float2 y = ffma2(make_float2(w[e], w[e + 1]), make_float2(inv, inv), make_float2(l[h], l[h + 1]));
-              l[h] = y.x;
-              l[h + 1] = y.y;
+              ln[h] = y.x;
+              ln[h + 1] = y.y;
             }
+            uint32_t a0, b0, a1, b1;
             split2(w[0], w[1], a0, b0);
             split2(w[2], w[3], a1, b1);
             wh[i] = a0 | (a1 << 16);
             wl[i] = b0 | (b1 << 16);
           }
-          const uint32_t at = r * 64 + (((grp * 2 + q) ^ ((r >> 1) & 3)) << 4);
-          *reinterpret_cast<uint4*>(&S.rows[b].rope[at]) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-          *reinterpret_cast<uint4*>(&S.w_lo[at]) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+        };
+        logits();
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < kGH; ++i) top = fmaxf(top, x[i]);
+        // the group's vote on moving the reference; the weights are worked out meanwhile
+        const bool usable = s > 0.f;
+        const bool over = __any_sync(0xffffffffu, seen ? top > kLimit : usable);
+        if (lane == 0) {
+          if (over) S.over[grp][b] = 1;
+          mbar_arrive(&S.vote[grp]);
         }
-        fence_proxy_async_smem();
+        weights();
+        bad |= !wait(&S.vote[grp], g & 1, p.status, ab);
+        bad |= g > 0 && !wait(&S.rows_empty[b ^ 1][quad], ((g - 1) >> 1) & 1, p.status, ab);   // W_lo is free
+        if ((bad = __any_sync(0xffffffffu, bad))) break;
+        if (*const_cast<volatile int*>(&S.over[grp][b])) {
+          // move the reference of the heads that need it (all of them at the first usable rows)
+          float v[kGH];
+#pragma unroll
+          for (int i = 0; i < kGH; ++i) v[i] = usable ? x[i] : -INFINITY;
+          const float mine = reduce_transposed<true>(v, lane);
+          if (lane < kGH) S.red[grp][quad][lane] = mine;
+          bad |= !meet(&S.sync[grp], met, lane, p.status, ab);
+          const int hl = lane & (kGH - 1);
+          const float mx =
+              fmaxf(fmaxf(S.red[grp][0][hl], S.red[grp][1][hl]), fmaxf(S.red[grp][2][hl], S.red[grp][3][hl]));
+          const float up = (seen ? mx > kLimit : mx > -INFINITY) ? mx - kTop : 0.f;
+          const float f = seen ? ex2_approx(-up) : 1.f;   // of head 16 grp + lane mod 16
+          if (seen) {
+            // O so far: wait for the product of the tile before this one
+            bad |= !wait(&S.rows_empty[b ^ 1][3], ((g - 1) >> 1) & 1, p.status, ab);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int mt = 0; mt < 4; ++mt) {
+              uint32_t o[16];
+              tmem_ld16(o_at + mt * kHT, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < kGH; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xffffffffu, f, i));
+              tmem_st16(o_at + mt * kHT, o);
+            }
+            tmem_st_wait();
+          }
+#pragma unroll
+          for (int i = 0; i < kGH; ++i) {
+            x[i] -= __shfl_sync(0xffffffffu, up, i);
+            l[i] *= __shfl_sync(0xffffffffu, f, i);
+          }
+          if (quad == 0) {
+            if (lane < kGH) S.m[grp * kGH + lane] += up;
+            if (lane == 0) S.over[grp][b] = 0;
+          }
+          seen = true;
+          weights();
+          bad |= !meet(&S.sync[grp], met, lane, p.status, ab);   // m is set, red may be reused
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.w_full);
+        if (lane == 0) mbar_arrive(&S.s_free[b]);
+#pragma unroll
+        for (int i = 0; i < kGH; ++i) l[i] = ln[i];
+        const uint32_t at = r * 64 + ((grp ^ ((r >> 1) & 3)) << 4);
+        *reinterpret_cast<uint4*>(&S.rows[b].rope[at]) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+        *reinterpret_cast<uint4*>(&S.w_lo[at]) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.w_full[quad]);
       }
-      if (stop) break;
+      if ((bad = __any_sync(0xffffffffu, bad))) break;
+      if (it + step < p.items) next_queries(kk + 1, it + step);
       // denominators: over the warp's rows, then over the four warps
-      S.red[grp][quad][lane] = reduce_transposed<false>(l, lane);
-      if (bar_or(kBarSoft + grp, 128, bad)) break;
-      const float total = (S.red[grp][0][lane] + S.red[grp][1][lane]) + (S.red[grp][2][lane] + S.red[grp][3][lane]);
+      const float mine = reduce_transposed<false>(l, lane);
+      if (lane < kGH) S.red[grp][quad][lane] = mine;
+      bad |= !meet(&S.sync[grp], met, lane, p.status, ab);
+      const int hl = lane & (kGH - 1);
+      const float total = (S.red[grp][0][hl] + S.red[grp][1][hl]) + (S.red[grp][2][hl] + S.red[grp][3][hl]);
       const float inv_l = total == 0.f ? 0.f : 1.f / total;
       const int64_t row = p.splits == 1 ? static_cast<int64_t>(I.t) * p.H
                                         : (static_cast<int64_t>(I.t) * p.splits + I.sp) * p.H;
-      if (quad == 0 && h0 + lane < p.H) {
-        const float lse = total == 0.f ? -INFINITY : (S.m[grp * 32 + lane] + log2f(total)) * 0.6931471805599453f;
-        if (p.splits > 1)
-          p.part_lse[row + h0 + lane] = lse;
-        else if (p.lse)
-          p.lse[row + h0 + lane] = lse;
+      if (quad == 0 && lane < kGH) {
+        const float lse = total == 0.f ? -INFINITY : (S.m[grp * kGH + lane] + log2f(total)) * 0.6931471805599453f;
+        S.m[grp * kGH + lane] = 0.f;                // for the next item
+        if (h0 + lane < p.H) {
+          if (p.splits > 1)
+            p.part_lse[row + h0 + lane] = lse;
+          else if (p.lse)
+            p.lse[row + h0 + lane] = lse;
+        }
       }
-      named_bar_sync(kBarSoft + grp, 128);          // red and m may be reused
-      if (tiles > 0) {
-        bad |= !wait(&S.o_full, items_done & 1, p.status, ab);
-        __syncwarp();
-        tc_fence_after();
-        ++items_done;
-      }
+      bad |= !meet(&S.sync[grp], met, lane, p.status, ab);       // red may be reused, m is reset
+      if (tiles > 0) bad |= !wait(&S.o_full, (nq - 1) & 1, p.status, ab);
+      if ((bad = __any_sync(0xffffffffu, bad))) break;
       if (p.splits > 1 && tiles == 0) continue;     // the combine skips parts of weight 0
+      tc_fence_after();
+      float iv[kGH];
+#pragma unroll
+      for (int i = 0; i < kGH; ++i) iv[i] = __shfl_sync(0xffffffffu, inv_l, i);
+      // Lanes hold neighbouring dims of every head: a pair of lanes trades, so that the even
+      // one has two dims of an even head and the odd one two dims of the odd head after it.
+      const int odd = lane & 1;
 #pragma unroll 1
-      for (int q = 0; q < 8; ++q) {
-        const int mt = q >> 1, hc = (q & 1) * 16;
+      for (int mt = 0; mt < 4; ++mt) {
         uint32_t o[16];
         if (tiles > 0) {
-          tmem_ld16(tmem + lanes + kOCol + mt * 64 + grp * 32 + hc, o);
+          tmem_ld16(o_at + mt * kHT, o);
           tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = 0;
+          for (int i = 0; i < kGH; ++i) o[i] = 0;
         }
+        const int64_t at0 = (row + h0 + odd) * DSA_D_V + mt * 128 + r - odd;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float y = __uint_as_float(o[i]) * __shfl_sync(0xffffffffu, inv_l, hc + i);
-          const int h = h0 + hc + i;
-          if (h < p.H) {
-            const int64_t at = (row + h) * DSA_D_V + mt * 128 + r;
-            if (p.splits > 1)
-              p.part_o[at] = y;
-            else
-              p.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        for (int i = 0; i < kGH; i += 2) {
+          const float a = __uint_as_float(o[i]) * iv[i], c = __uint_as_float(o[i + 1]) * iv[i + 1];
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
+          const float d0 = odd ? got : a, d1 = odd ? c : got;
+          if (h0 + i < p.H) {                       // H is even
+            if (p.splits > 1) {
+              *reinterpret_cast<float2*>(p.part_o + at0 + i * DSA_D_V) = make_float2(d0, d1);
+            } else {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(d0, d1);
+              *reinterpret_cast<uint32_t*>(p.out + at0 + i * DSA_D_V) = *reinterpret_cast<const uint32_t*>(&y);
+            }
           }
         }
       }
@@ -402,48 +512,18 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       }
     }
   } else if (warp < kSoftWarps + kGatherWarps) {
-    // ================================================================ queries and rows
+    // ================================================================ rows
     setmaxnreg_dec<kGatherRegs>();
     const int gw = warp - kSoftWarps, gt = tid - 32 * kSoftWarps;
-    uint32_t g = 0, nq = 0;
-    int prev_tiles = 0;                             // of the last non-empty item
-    bool bad = false;                               // a wait of this thread ran out
-    for (int kk = 0, it = blockIdx.x; it < p.items; ++kk, it += step) {
+    uint32_t g = 0, met = 0;
+    bool bad = false;                               // a wait ran out
+    for (int kk = 0, it = blockIdx.x; it < p.items && !bad; ++kk, it += step) {
       Item I;
       item_place(p, it, I);
       item_list(p, I);
       if (!I.ok && gt == 0) set_status(p.status, DSA_DEV_BAD_QUERY);
-      // tiles up to the last usable entry
       int tiles = I.e1 > I.e0 ? (I.e1 - I.e0 + kRows - 1) / kRows : 0;
       const int32_t* list = p.idx ? p.idx + static_cast<int64_t>(I.t) * p.k : nullptr;
-      if (!list && __any_sync(0xffffffffu, bad)) break;
-      if (list && tiles > 0) {
-        int v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = I.e0 + i * 256 + gt;
-          v[i] = e < I.e1 ? __ldg(list + e) : -1;
-        }
-        int last = -1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (v[i] >= I.len) set_status(p.status, DSA_DEV_BAD_INDEX);
-          if (v[i] >= 0 && v[i] < I.len) last = i * 256 + gt;
-        }
-        last = __reduce_max_sync(0xffffffffu, last);
-        if (lane == 0) S.last[gw] = last;
-        if (bar_or(kBarGather, 32 * kGatherWarps, bad)) break;
-#pragma unroll
-        for (int i = 0; i < kGatherWarps; ++i) last = max(last, S.last[i]);
-        tiles = last / kRows + (last >= 0 ? 1 : 0);
-        named_bar_sync(kBarGather, 32 * kGatherWarps);
-      }
-      if (gt == 0) {
-        bad |= kk > 1 && !wait(&S.plan_free[kk & 1], ((kk - 2) >> 1) & 1, p.status, ab);
-        S.plan[kk & 1] = tiles;
-        mbar_arrive(&S.plan_full[kk & 1]);
-      }
-      if (tiles == 0) continue;
       // the lane's entries: lanes 0-15 rows 16 gw .. of the pair's first tile, 16-31 of its second
       auto entry = [&](int pair) {
         const int e = I.e0 + (2 * pair + (lane >> 4)) * kRows + gw * 16 + (lane & 15);
@@ -465,56 +545,39 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         return static_cast<int>(row);
       };
       auto scale_of = [&](int row) { return row >= 0 ? __ldg(p.scale + (row >> p.block_log2)) : 0.f; };
-      int v_cur = entry(0), v_nxt = entry(1);
-
-      // the item's queries, once the products of the last item have read its own; qs has
-      // two places, so the softmax must be through with the item before that (it is,
-      // unless the last item was a single tile, whose product may run ahead of it)
-      bad |= nq > 0 && !wait(&S.q_free, (nq - 1) & 1, p.status, ab);
-      if (prev_tiles == 1 && nq > 1) bad |= !wait(&S.s_free[g & 1], ((g - 2) >> 1) & 1, p.status, ab);
-      prev_tiles = tiles;
-      for (int hl = gw; hl < kHT; hl += kGatherWarps) {
-        const int h = I.hg * kHT + hl;
-        uint32_t w[9];
-        const uint32_t* src =
-            reinterpret_cast<const uint32_t*>(p.q + (static_cast<int64_t>(I.t) * p.H + h) * DSA_D_QK);
+      const int v_cur = entry(0);
+      int v_nxt = entry(1);
+      // tiles up to the last usable entry
+      if (list && tiles > 0) {
+        int v[8];
 #pragma unroll
-        for (int i = 0; i < 9; ++i) w[i] = h < p.H ? __ldg(src + i * 32 + lane) : 0u;
-        uint32_t am = 0;
-#pragma unroll
-        for (int i = 0; i < 9; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-        am = __reduce_max_sync(0xffffffffu, am);
-        // times 2^e: the largest entry in [2^7, 2^8)
-        int e = am >= 0x80u ? 7 + 127 - static_cast<int>(am >> 7) : 120;
-        e = e > 120 ? 120 : (e < -120 ? -120 : e);
-        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-        if (lane == 0) S.qs[nq & 1][hl] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < 9; ++i) {
-          uint32_t hi, lo;
-          split2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up, hi, lo);
-          if (am >= 0x7f80u) hi = 0x7f7fu;          // an infinity or NaN: the head's results are NaN
-          const int byte = 2 * (lane + 32 * i);
-          if (i < 8) {
-            const uint32_t at = (((byte & 127) >> 4) ^ (hl & 7)) * 16 + (byte & 15);
-            *reinterpret_cast<uint16_t*>(&S.q.lat[i >> 1][hl * 128 + at]) = static_cast<uint16_t>(hi);
-            *reinterpret_cast<uint16_t*>(&S.q.lat[i >> 1][(hl + kHT) * 128 + at]) = static_cast<uint16_t>(lo);
-          } else {
-            const uint32_t at = (((byte & 63) >> 4) ^ ((hl >> 1) & 3)) * 16 + (byte & 15);
-            *reinterpret_cast<uint16_t*>(&S.q.rope[hl * 64 + at]) = static_cast<uint16_t>(hi);
-            *reinterpret_cast<uint16_t*>(&S.q.rope[(hl + kHT) * 64 + at]) = static_cast<uint16_t>(lo);
-          }
+        for (int i = 0; i < 8; ++i) {
+          const int e = I.e0 + i * 256 + gt;
+          v[i] = e < I.e1 ? __ldg(list + e) : -1;
         }
+        int last = -1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (v[i] >= I.len) set_status(p.status, DSA_DEV_BAD_INDEX);
+          if (v[i] >= 0 && v[i] < I.len) last = i * 256 + gt;
+        }
+        last = __reduce_max_sync(0xffffffffu, last);
+        if (lane == 0) S.last[gw] = last;
+        bad |= !meet(&S.gather_sync, met, lane, p.status, ab);
+#pragma unroll
+        for (int i = 0; i < kGatherWarps; ++i) last = max(last, S.last[i]);
+        tiles = last / kRows + (last >= 0 ? 1 : 0);
+        bad |= !meet(&S.gather_sync, met, lane, p.status, ab);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.q_full);
-      ++nq;
-
-      // rows, tile by tile; the next pair's page, row and scale are looked up meanwhile
       int row = place(v_cur, page(v_cur));
+      if (gt == 0) {
+        bad |= kk > 1 && !wait(&S.plan_free[kk & 1], ((kk - 2) >> 1) & 1, p.status, ab);
+        S.plan[kk & 1] = tiles;
+        mbar_arrive(&S.plan_full[kk & 1]);
+      }
       float sc = scale_of(row);
       int pg_nxt = page(v_nxt);
+      // tile by tile; the next pair's page, row and scale are looked up meanwhile
       for (int j = 0; j < tiles; ++j, ++g) {
         if (!(sc >= 7.888609e-31f && sc <= 1.2676506e30f)) {   // 2^-100 .. 2^100
           if (row >= 0) set_status(p.status, DSA_DEV_BAD_SCALE);
@@ -522,8 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
           sc = 0.f;
         }
         const int b = g & 1, half = j & 1;
-        bad |= g > 1 && !wait(&S.rows_empty[b], ((g - 2) >> 1) & 1, p.status, ab);
-        if (__any_sync(0xffffffffu, bad)) break;
+        bad |= g > 1 && !wait(&S.rows_empty[b][gw >> 1], ((g - 2) >> 1) & 1, p.status, ab);
+        if ((bad = __any_sync(0xffffffffu, bad))) break;
         const uint32_t lat = smem_u32(S.rows[b].lat[0]) + (lane >> 3) * (kRows * 128);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -551,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
           pg_nxt = page(v_nxt);
         }
       }
+      bad = __any_sync(0xffffffffu, bad);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
@@ -572,8 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         for (int j = 0; j < tiles; ++j, ++g) {
           const int b = g & 1;
           const uint32_t ph = (g >> 1) & 1;
-          if ((g > 1 && !wait(&S.s_free[b], ph ^ 1, p.status, ab)) ||
-              !wait(&S.rows_full[b], ph, p.status, ab)) {
+          if ((g > 1 && !wait(&S.s_free[b], ph ^ 1, p.status, ab)) || !wait(&S.rows_full[b], ph, p.status, ab)) {
             ok = false;
             break;
           }
@@ -610,29 +673,25 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         if (tiles == 0) continue;
         if (no > 0 && !wait(&S.o_free, (no - 1) & 1, p.status, ab)) break;
         ++no;
-        for (int j = 0; j < tiles; ++j, ++g) {
+        for (int j = 0; j < tiles && ok; ++j, ++g) {
           const int b = g & 1;
-          if (!wait(&S.w_full, g & 1, p.status, ab)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
           const uint64_t a = smem_desc_sw128(smem_u32(S.rows[b].lat[0]), 16, 1024);
           const uint64_t w_hi = smem_desc_sw64(smem_u32(S.rows[b].rope), 512);
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt)
+          for (int k = 0; k < 4; ++k) {
+            if (!wait(&S.w_full[k], g & 1, p.status, ab)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f8(tmem + kOCol + mt * 64, a + mt * (kRows * 128 / 16) + k * (32 * 128 / 16),
-                      w_lo + k * (32 * 64 / 16), id, (j | k) != 0 ? 1u : 0u);
-          umma_commit(&S.wlo_free);
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f8(tmem + kOCol + mt * 64, a + mt * (kRows * 128 / 16) + k * (32 * 128 / 16),
-                      w_hi + k * (32 * 64 / 16), id, 1u);
-          umma_commit(&S.rows_empty[b]);
+            for (int mt = 0; mt < 4; ++mt) {
+              const uint64_t am = a + mt * (kRows * 128 / 16) + k * (32 * 128 / 16);
+              umma_f8(tmem + kOCol + mt * kHT, am, w_lo + k * (32 * 64 / 16), id, (j | k) != 0 ? 1u : 0u);
+              umma_f8(tmem + kOCol + mt * kHT, am, w_hi + k * (32 * 64 / 16), id, 1u);
+            }
+            umma_commit(&S.rows_empty[b][k]);
+          }
         }
         if (!ok) break;
         umma_commit(&S.o_full);
