@@ -25,9 +25,10 @@
 // the row tile's RoPE part, which only the first product reads.  The second product
 // goes by quarters of 32 rows (one K step, all dims, lo and hi), each of which gives
 // its rows and weights back, so the next tile's rows and weights follow it closely.
-// 28 warps: 0-15 softmax, output and the next queries' hi/lo split (warp w: rows
-// 32 (w mod 4) .., 16 heads), 16-23 row gathers (16-byte cp.async), 24 issues S^T, 25
-// O^T.  Registers: launched at 72 per thread, softmax 88, gathers 56, issuers 40.
+// 32 warps: 0-15 softmax (warp w: rows 32 (w mod 4) .., 16 heads) and, between items,
+// the next queries' hi/lo split, 16-23 row gathers (16-byte cp.async), 24-27 the
+// output (while the softmax is at the next item), 28 issues S^T, 29 O^T.  Registers:
+// launched at 64 per thread, softmax 80, gathers 56, output 48, issuers 32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -45,13 +46,16 @@ constexpr int kSoftWarps = 16;
 constexpr int kGroups = kSoftWarps / 4;            // softmax groups of four warps (128 rows)
 constexpr int kGH = kHT / kGroups;                 // heads per group
 constexpr int kGatherWarps = 8;
-constexpr int kThreads = 32 * (kSoftWarps + kGatherWarps + 4);
-constexpr int kLaunchRegs = 72, kSoftRegs = 88, kGatherRegs = 56, kIssueRegs = 40;
-static_assert(32 * (kSoftWarps * kSoftRegs + kGatherWarps * kGatherRegs + 4 * kIssueRegs) == kThreads * kLaunchRegs,
+constexpr int kOutWarps = 4;
+constexpr int kThreads = 32 * (kSoftWarps + kGatherWarps + kOutWarps + 4);
+constexpr int kLaunchRegs = 64, kSoftRegs = 80, kGatherRegs = 56, kOutRegs = 48, kIssueRegs = 32;
+static_assert(32 * (kSoftWarps * kSoftRegs + kGatherWarps * kGatherRegs + kOutWarps * kOutRegs + 4 * kIssueRegs) ==
+                  kThreads * kLaunchRegs,
               "the register split must add up to the launch allocation");
 constexpr uint32_t kSCol = 0, kOCol = 256;         // TMEM columns
-constexpr float kTop = 5.f;                        // log2 of the largest weight when m is set
-constexpr float kLimit = 8.5f;                     // log2 of the weight that makes m move
+// Weights are held as w / 2^8 until their codes are formed (see split4).
+constexpr float kTop = 5.f - 8.f;                  // log2 of the largest weight when m is set
+constexpr float kLimit = 8.5f - 8.f;               // log2 of the weight that makes m move
 constexpr int kMaxSplits = 64;
 
 struct Tile {                                      // 128 rows: latent as 4 x 128 B (SW128), RoPE 64 B (SW64)
@@ -66,8 +70,8 @@ struct Q8Smem {
   float s_row[2][kRows];                           // row scales, 0 = unused row
   float red[kGroups][4][kGH];
   uint16_t qs[2][kHT];                             // 2^-e of each head's query, bf16
-  float m[kHT];
-  uint64_t rows_full[2], rows_empty[2][4], s_full[2], s_free[2], w_full[4], q_full, q_free, o_full, o_free,
+  float m[kHT];                                    // minus the references
+  uint64_t rows_full[2], rows_empty[2][4], s_full[2], s_free[2], w_full[4], q_full, q_free, o_full, o_free, l_full, l_free,
       plan_full[2], plan_free[2], vote[kGroups], sync[kGroups], gather_sync, done;
   int over[kGroups][2];                            // a weight of the group passed the limit (by tile parity)
   int plan[2];                                     // tiles of the item
@@ -77,14 +81,30 @@ struct Q8Smem {
 };
 static_assert(sizeof(Q8Smem) <= 232448, "exceeds the 227 KB a CTA can have");
 
-__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t sbo_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(1) << 16;
-  d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
-  d |= 1ull << 46;   // descriptor version (sm_100)
-  d |= 4ull << 61;   // SWIZZLE_64B
-  return d;
+// Every warpgroup calls this first thing in its role: an increase waits until the
+// others have given back enough of the launch allocation.
+template <int N>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (N > kLaunchRegs) setmaxnreg_inc<N>();
+  if constexpr (N < kLaunchRegs) setmaxnreg_dec<N>();
+}
+
+// Upper words of the operands' descriptors (8-row groups 1024 and 512 bytes apart;
+// descriptor version, swizzle); the lower word is the start address over 16.
+constexpr uint32_t kDesc128 = (1024u >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t kDesc64 = (512u >> 4) | 1u << 14 | 4u << 29;
+__device__ __forceinline__ uint32_t desc_lo(const void* p) { return ((smem_u32(p) >> 4) & 0x3fffu) | 1u << 16; }
+
+// D[tmem] (+)= A . B, E4M3 operands.
+template <uint32_t kDescA, uint32_t kDescB>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "n"(kDescA), "r"(b), "n"(kDescB), "r"(id), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -93,19 +113,31 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Two fp32 -> E4M3 hi and lo with hi + lo = the value to 8 significant bits (low byte
-// = a).  Through fp16, which holds 11 bits: |x| <= 448 and steps of 2^-24 near zero,
-// both beyond what hi and lo can hold.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  uint32_t x, h, r;
-  uint16_t hb, lb;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hb) : "r"(x));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(hb));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(h));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lb) : "r"(r));
-  hi = hb;
-  lo = lb;
+// Four fp32 values of magnitude below 2 -> E4M3 codes of hi and lo, hi + lo = 2^8 times
+// the value to 8 significant bits (byte i = value i).  By way of fp16: with the 2^8
+// taken off, E4M3's exponent field equals fp16's low four exponent bits, its
+// subnormals start where fp16's do, and a code is bits 7 .. 14 of the fp16 pattern
+// (bit 14 is 0 below 2).  So hi is the pattern cut after 3 mantissa bits, lo the
+// exact rest rounded to 3, and both come from integer operations (the E4M3
+// conversion instructions run at a sixteenth of their rate).  NaN stays NaN in hi.
+template <bool kSigned>
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+  uint32_t x0, x1, r0, r1;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x0) : "f"(b), "f"(a));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x1) : "f"(d), "f"(c));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(x0), "r"(x0 & 0xff80ff80u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(x1), "r"(x1 & 0xff80ff80u));
+  r0 += 0x00400040u;
+  r1 += 0x00400040u;
+  uint32_t h0 = x0 << 1, h1 = x1 << 1, l0 = r0 << 1, l1 = r1 << 1;
+  if (kSigned) {
+    h0 |= x0 & 0x80008000u;
+    h1 |= x1 & 0x80008000u;
+    l0 |= r0 & 0x80008000u;
+    l1 |= r1 & 0x80008000u;
+  }
+  hi = __byte_perm(h0, h1, 0x7531);
+  lo = __byte_perm(l0, l1, 0x7531);
 }
 
 // Bounded wait that gives up at once when a thread of the CTA has given up.  Warps
@@ -125,9 +157,33 @@ __device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& phase, int lane, u
   return ok;
 }
 
+// Packed fp32 pairs, each lane rounded like the scalar operation.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {   // one ulp; exact for powers of two
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -182,52 +238,57 @@ __device__ __forceinline__ void item_list(const MlaQ8Params& p, Item& I) {
   I.e1 = I.ok ? min(n, I.e0 + p.split_tiles * kRows) : I.e0;
 }
 
-// Splits the 64 heads' queries of an item into hi and lo (this warp: heads warp + 16 i)
-// and stores them as the first product's operand.
-__device__ __forceinline__ void split_queries(const MlaQ8Params& p, Q8Smem& S, int t, int hg, uint32_t slot, int warp,
+// Splits the 64 heads' queries of an item into hi and lo (this warp: heads w0 + 16 i) and
+// stores them as the first product's operand.  A lane takes 4 neighbouring entries
+// of each 128 (and lanes 0-15 4 of the last 64).
+__device__ __forceinline__ void split_queries(const MlaQ8Params& p, Q8Smem& S, int t, int hg, uint32_t slot, int w0,
                                               int lane) {
-#pragma unroll 1
-  for (int i0 = 0; i0 < kHT / kSoftWarps; i0 += 2) {
-    uint32_t w[2][9];
+  const uint2* src0 =
+      reinterpret_cast<const uint2*>(p.q + (static_cast<int64_t>(t) * p.H + hg * kHT) * DSA_D_QK) + lane;
+  const int heads = min(kHT, p.H - hg * kHT);
+  auto load = [&](int hl, uint2(&v)[5]) {
+    const uint2* src = src0 + hl * (DSA_D_QK / 4);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int h = hg * kHT + warp + (i0 + u) * kSoftWarps;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (static_cast<int64_t>(t) * p.H + h) * DSA_D_QK);
+    for (int i = 0; i < 5; ++i)
+      v[i] = hl < heads && (i < 4 || lane < 16) ? __ldg(src + i * 32) : make_uint2(0u, 0u);
+  };
+  auto split = [&](int hl, const uint2(&v)[5]) {
+    uint32_t am = 0;                                // two 16-bit maxima
 #pragma unroll
-      for (int i = 0; i < 9; ++i) w[u][i] = h < p.H ? __ldg(src + i * 32 + lane) : 0u;
-    }
+    for (int i = 0; i < 5; ++i) am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu));
+    am = __reduce_max_sync(0xffffffffu, max(am & 0xffffu, am >> 16));
+    // times 2^e: the largest entry in [2^-1, 1)
+    int e = 126 - static_cast<int>(am >> 7);
+    if (e > 118) e = 118;
+    const float up = __uint_as_float(e >= -126 ? static_cast<uint32_t>(e + 127) << 23 : 0x00800000u >> (-126 - e));
+    if (lane == 0) S.qs[slot][hl] = static_cast<uint16_t>((119 - e) << 7);   // 2^-(e + 8)
+    const bool bad = am >= 0x7f80u;                 // an infinity or NaN: the head's results are NaN
+    uint8_t* lat = &S.q.lat[0][hl * 128 + ((lane >> 2) ^ (hl & 7)) * 16 + (lane & 3) * 4];
+    uint8_t* rope = &S.q.rope[hl * 64 + (((lane >> 2) & 3) ^ ((hl >> 1) & 3)) * 16 + (lane & 3) * 4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int hl = warp + (i0 + u) * kSoftWarps;
-      uint32_t am = 0;
-#pragma unroll
-      for (int i = 0; i < 9; ++i) am = max(am, max(w[u][i] & 0x7fffu, (w[u][i] >> 16) & 0x7fffu));
-      am = __reduce_max_sync(0xffffffffu, am);
-      // times 2^e: the largest entry in [2^7, 2^8)
-      int e = am >= 0x80u ? 7 + 127 - static_cast<int>(am >> 7) : 120;
-      e = e > 120 ? 120 : (e < -120 ? -120 : e);
-      const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      if (lane == 0) S.qs[slot][hl] = static_cast<uint16_t>((127 - e) << 7);
-      const bool bad = am >= 0x7f80u;               // an infinity or NaN: the head's results are NaN
-      uint8_t* lat = &S.q.lat[0][hl * 128];
-      const uint32_t col = 2 * lane & 63;           // bytes 64 i + 2 lane of the row
-#pragma unroll
-      for (int i = 0; i < 9; ++i) {
-        uint32_t hi, lo;
-        split2(__uint_as_float(w[u][i] << 16) * up, __uint_as_float(w[u][i] & 0xffff0000u) * up, hi, lo);
-        if (bad) hi = 0x7f7fu;
-        if (i < 8) {
-          const uint32_t at = (((col >> 4) + (i & 1) * 4) ^ (hl & 7)) * 16 + (col & 15) + (i >> 1) * (kRows * 128);
-          *reinterpret_cast<uint16_t*>(lat + at) = static_cast<uint16_t>(hi);
-          *reinterpret_cast<uint16_t*>(lat + at + kHT * 128) = static_cast<uint16_t>(lo);
-        } else {
-          const uint32_t at = hl * 64 + ((col >> 4) ^ ((hl >> 1) & 3)) * 16 + (col & 15);
-          *reinterpret_cast<uint16_t*>(&S.q.rope[at]) = static_cast<uint16_t>(hi);
-          *reinterpret_cast<uint16_t*>(&S.q.rope[at + kHT * 64]) = static_cast<uint16_t>(lo);
-        }
+    for (int i = 0; i < 5; ++i) {
+      const float2 a = mul2(make_float2(__uint_as_float(v[i].x << 16), __uint_as_float(v[i].x & 0xffff0000u)),
+                            make_float2(up, up));
+      const float2 b = mul2(make_float2(__uint_as_float(v[i].y << 16), __uint_as_float(v[i].y & 0xffff0000u)),
+                            make_float2(up, up));
+      uint32_t hi, lo;
+      split4<true>(a.x, a.y, b.x, b.y, hi, lo);
+      if (bad) hi = 0x7f7f7f7fu;
+      if (i < 4) {
+        *reinterpret_cast<uint32_t*>(lat + i * (kRows * 128)) = hi;
+        *reinterpret_cast<uint32_t*>(lat + i * (kRows * 128) + kHT * 128) = lo;
+      } else if (lane < 16) {
+        *reinterpret_cast<uint32_t*>(rope) = hi;
+        *reinterpret_cast<uint32_t*>(rope + kHT * 64) = lo;
       }
     }
-  }
+  };
+  constexpr int kPer = kHT / kSoftWarps;
+  uint2 w[kPer][5];                                 // all loads in flight
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) load(w0 + i * kSoftWarps, w[i]);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) split(w0 + i * kSoftWarps, w[i]);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(&S.q_full);
@@ -249,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       mbar_init(&S.s_full[b], 1);
       mbar_init(&S.s_free[b], kSoftWarps);
       mbar_init(&S.plan_full[b], 1);
-      mbar_init(&S.plan_free[b], kSoftWarps + 2);
+      mbar_init(&S.plan_free[b], kSoftWarps + kOutWarps + 2);
       for (int k = 0; k < 4; ++k) mbar_init(&S.rows_empty[b][k], 1);
     }
     for (int k = 0; k < 4; ++k) mbar_init(&S.w_full[k], kGroups);
@@ -262,12 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     mbar_init(&S.q_full, kSoftWarps);
     mbar_init(&S.q_free, 1);
     mbar_init(&S.o_full, 1);
-    mbar_init(&S.o_free, kSoftWarps);
+    mbar_init(&S.o_free, kOutWarps);
+    mbar_init(&S.l_full, kSoftWarps);
+    mbar_init(&S.l_free, kOutWarps);
     mbar_init(&S.done, 2);
     fence_mbar_init();
   }
-  if (tid < kHT) S.m[tid] = 0.f;
-  if (warp == kSoftWarps + kGatherWarps) tmem_alloc(&S.tmem, 512);
+  if (warp == kSoftWarps + kGatherWarps + kOutWarps) tmem_alloc(&S.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -275,16 +337,16 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
   const int step = gridDim.x;
 
   if (warp < kSoftWarps) {
-    // ================================================================ softmax, output, queries
-    setmaxnreg_inc<kSoftRegs>();
+    // ================================================================ softmax
+    set_regs<kSoftRegs>();
     const int grp = warp >> 2, quad = warp & 3;     // heads 16 grp .., rows 32 quad ..
     const int r = quad * 32 + lane;
     const uint32_t s_at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kSCol + grp * kGH;
     const uint32_t o_at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kOCol + grp * kGH;
     const float c0 = p.sm_scale * 1.4426950408889634f;
-    uint32_t g = 0, nq = 0, met = 0;                // tiles, non-empty items, meetings of the group so far
+    uint32_t g = 0, nq = 0, met = 0, votes = 0;     // tiles, non-empty items, meetings, votes so far
     bool bad = false;                               // a wait ran out
-    int tiles = 0, tiles_next = 0, tiles_last = 0;  // of this item, the next, the last non-empty one
+    int tiles_next = 0, tiles_last = 0;             // tiles of the next item, of the last non-empty one
     // the tiles of the kk-th item, and its queries' operand if it has any
     auto next_queries = [&](int kk, int it) {
       bad |= !wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
@@ -292,9 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
       if (tiles_next == 0) return;
+      // the products of the last item have read its queries
       bad |= nq > 0 && !wait(&S.q_free, (nq - 1) & 1, p.status, ab);
-      // qs has two places: every warp must be through with the logits of the item before
-      // the last one (it is, unless the last one's only tile may have run ahead)
+      // qs has two places: every warp must be through with the logits of the item before the
+      // last one (it is, unless the last one's only tile may have run ahead)
       if (tiles_last == 1 && g > 1) bad |= !wait(&S.s_free[g & 1], ((g - 2) >> 1) & 1, p.status, ab);
       __syncwarp();
       Item I;
@@ -303,18 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     };
     if (blockIdx.x < p.items) next_queries(0, blockIdx.x);
     for (int kk = 0, it = blockIdx.x; it < p.items; ++kk, it += step) {
-      Item I;
-      item_place(p, it, I);
-      tiles = tiles_next;
-      if (it + step < p.items) {                    // the next item's queries on their way to L2
-        Item N;
-        item_place(p, it + step, N);
-        const int h0 = N.hg * kHT, lines = min(kHT, p.H - h0) * 9;
-        const char* src = reinterpret_cast<const char*>(p.q + (static_cast<int64_t>(N.t) * p.H + h0) * DSA_D_QK);
-        for (int i = tid; i < lines; i += 32 * kSoftWarps)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i * 128));
-      }
-      const int h0 = I.hg * kHT + grp * kGH;
+      const int tiles = tiles_next;
       const uint32_t slot = nq & 1;
       float l[kGH];
 #pragma unroll
@@ -332,13 +384,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         if ((bad = __any_sync(0xffffffffu, bad))) break;
         tc_fence_after();
         const float s = S.s_row[b][r];
+        const bool usable = s > 0.f;
         const float c = c0 * s;
-        const float sg = s > 0.f ? lg2_approx(s) : -INFINITY;
-        const float inv = s > 0.f ? 1.f / s : 0.f;
+        const float sg = usable ? lg2_approx(s) : -INFINITY;
+        const float inv = usable ? rcp_approx(s) : 0.f;
         uint32_t wh[4], wl[4];
-        float ln[kGH];
-        // x = b - m, the log2 of the weight; the weights, split, and the denominators with them
-        float x[kGH];
+        float x[kGH];                               // log2 of the weight, then the weight
         auto logits = [&]() {
           uint32_t hi[kGH], lo[kGH];
           tmem_ld16(s_at + b * 128, hi);
@@ -348,64 +399,69 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
           for (int i = 0; i < kGH; i += 2) {
             const uint32_t sc = *reinterpret_cast<const uint32_t*>(&S.qs[slot][grp * kGH + i]);
             const float2 mm = *reinterpret_cast<const float2*>(&S.m[grp * kGH + i]);
-            const float2 d = make_float2(__uint_as_float(hi[i]) + __uint_as_float(lo[i]),
-                                         __uint_as_float(hi[i + 1]) + __uint_as_float(lo[i + 1]));
-            const float2 y =
-                ffma2(d, make_float2(__uint_as_float(sc << 16) * c, __uint_as_float(sc & 0xffff0000u) * c),
-                      make_float2(sg - mm.x, sg - mm.y));
+            const float2 d = add2(make_float2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
+                                  make_float2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
+            const float2 k = mul2(make_float2(__uint_as_float(sc << 16), __uint_as_float(sc & 0xffff0000u)),
+                                  make_float2(c, c));
+            // an item's first logits have no reference yet
+            const float2 y = ffma2(d, k, seen ? add2(make_float2(sg, sg), mm) : make_float2(sg, sg));
             x[i] = y.x;
             x[i + 1] = y.y;
           }
         };
+        logits();
         auto weights = [&]() {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float w[4];
+          for (int i = 0; i < kGH; ++i) x[i] = ex2_approx(x[i]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = ex2_approx(x[i * 4 + e]);
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              const int h = i * 4 + e;
-              const float2 y = ffma2(make_float2(w[e], w[e + 1]), make_float2(inv, inv), make_float2(l[h], l[h + 1]));
-              ln[h] = y.x;
-              ln[h + 1] = y.y;
-            }
-            uint32_t a0, b0, a1, b1;
-            split2(w[0], w[1], a0, b0);
-            split2(w[2], w[3], a1, b1);
-            wh[i] = a0 | (a1 << 16);
-            wl[i] = b0 | (b1 << 16);
-          }
+          for (int i = 0; i < 4; ++i) split4<false>(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], wh[i], wl[i]);
         };
-        logits();
-        float top = x[0];
-#pragma unroll
-        for (int i = 1; i < kGH; ++i) top = fmaxf(top, x[i]);
-        // the group's vote on moving the reference; the weights are worked out meanwhile
-        const bool usable = s > 0.f;
-        const bool over = __any_sync(0xffffffffu, seen ? top > kLimit : usable);
-        if (lane == 0) {
-          if (over) S.over[grp][b] = 1;
-          mbar_arrive(&S.vote[grp]);
-        }
-        weights();
-        bad |= !wait(&S.vote[grp], g & 1, p.status, ab);
-        bad |= g > 0 && !wait(&S.rows_empty[b ^ 1][quad], ((g - 1) >> 1) & 1, p.status, ab);   // W_lo is free
-        if ((bad = __any_sync(0xffffffffu, bad))) break;
-        if (*const_cast<volatile int*>(&S.over[grp][b])) {
-          // move the reference of the heads that need it (all of them at the first usable rows)
+        // The largest logit over the group's 128 rows, of head 16 grp + lane mod 16 (of NaN
+        // only: -infinity).  red and m may still hold the last item's sums and references.
+        auto largest = [&]() {
           float v[kGH];
 #pragma unroll
           for (int i = 0; i < kGH; ++i) v[i] = usable ? x[i] : -INFINITY;
           const float mine = reduce_transposed<true>(v, lane);
+          if (nq > 1) bad |= !wait(&S.l_free, nq & 1, p.status, ab);
+          __syncwarp();
           if (lane < kGH) S.red[grp][quad][lane] = mine;
           bad |= !meet(&S.sync[grp], met, lane, p.status, ab);
           const int hl = lane & (kGH - 1);
-          const float mx =
-              fmaxf(fmaxf(S.red[grp][0][hl], S.red[grp][1][hl]), fmaxf(S.red[grp][2][hl], S.red[grp][3][hl]));
-          const float up = (seen ? mx > kLimit : mx > -INFINITY) ? mx - kTop : 0.f;
-          const float f = seen ? ex2_approx(-up) : 1.f;   // of head 16 grp + lane mod 16
-          if (seen) {
+          return fmaxf(fmaxf(S.red[grp][0][hl], S.red[grp][1][hl]), fmaxf(S.red[grp][2][hl], S.red[grp][3][hl]));
+        };
+        bool met_now = false;                       // red and m were used: meet again when done
+        if (!seen) {
+          // set the reference at the first usable rows
+          const float mx = largest();
+          const float up = fabsf(mx) < INFINITY ? mx - kTop : 0.f;
+          seen = __any_sync(0xffffffffu, mx > -INFINITY);
+          if (quad == 0 && lane < kGH) S.m[grp * kGH + lane] = -up;
+#pragma unroll
+          for (int i = 0; i < kGH; ++i) x[i] -= __shfl_sync(0xffffffffu, up, i);
+          weights();
+          met_now = true;
+          bad |= g > 0 && !wait(&S.rows_empty[b ^ 1][quad], ((g - 1) >> 1) & 1, p.status, ab);   // W_lo is free
+        } else {
+          float top = x[0];
+#pragma unroll
+          for (int i = 1; i < kGH; ++i) top = fmaxf(top, x[i]);
+          // the group's vote on moving the reference; the weights are worked out meanwhile
+          const bool over = __any_sync(0xffffffffu, top > kLimit);
+          if (lane == 0) {
+            if (over) S.over[grp][votes & 1] = 1;
+            mbar_arrive(&S.vote[grp]);
+          }
+          weights();
+          bad |= !wait(&S.vote[grp], votes & 1, p.status, ab);
+          bad |= !wait(&S.rows_empty[b ^ 1][quad], ((g - 1) >> 1) & 1, p.status, ab);
+          if ((bad = __any_sync(0xffffffffu, bad))) break;
+          if (*const_cast<volatile int*>(&S.over[grp][votes & 1])) {
+            // move the reference of the heads that need it
+            logits();
+            const float mx = largest();
+            const float up = fabsf(mx) < INFINITY && mx > kLimit ? mx - kTop : 0.f;
+            const float f = ex2_approx(-up);
             // O so far: wait for the product of the tile before this one
             bad |= !wait(&S.rows_empty[b ^ 1][3], ((g - 1) >> 1) & 1, p.status, ab);
             __syncwarp();
@@ -421,99 +477,51 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
               tmem_st16(o_at + mt * kHT, o);
             }
             tmem_st_wait();
-          }
 #pragma unroll
-          for (int i = 0; i < kGH; ++i) {
-            x[i] -= __shfl_sync(0xffffffffu, up, i);
-            l[i] *= __shfl_sync(0xffffffffu, f, i);
+            for (int i = 0; i < kGH; ++i) l[i] *= __shfl_sync(0xffffffffu, f, i);
+            if (quad == 0) {
+              if (lane < kGH) S.m[grp * kGH + lane] -= up;
+              if (lane == 0) S.over[grp][votes & 1] = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < kGH; ++i) x[i] -= __shfl_sync(0xffffffffu, up, i);
+            weights();
+            met_now = true;
           }
-          if (quad == 0) {
-            if (lane < kGH) S.m[grp * kGH + lane] += up;
-            if (lane == 0) S.over[grp][b] = 0;
-          }
-          seen = true;
-          weights();
-          bad |= !meet(&S.sync[grp], met, lane, p.status, ab);   // m is set, red may be reused
+          ++votes;
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.s_free[b]);
-#pragma unroll
-        for (int i = 0; i < kGH; ++i) l[i] = ln[i];
         const uint32_t at = r * 64 + ((grp ^ ((r >> 1) & 3)) << 4);
         *reinterpret_cast<uint4*>(&S.rows[b].rope[at]) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
         *reinterpret_cast<uint4*>(&S.w_lo[at]) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.w_full[quad]);
-      }
-      if ((bad = __any_sync(0xffffffffu, bad))) break;
-      if (it + step < p.items) next_queries(kk + 1, it + step);
-      // denominators: over the warp's rows, then over the four warps
-      const float mine = reduce_transposed<false>(l, lane);
-      if (lane < kGH) S.red[grp][quad][lane] = mine;
-      bad |= !meet(&S.sync[grp], met, lane, p.status, ab);
-      const int hl = lane & (kGH - 1);
-      const float total = (S.red[grp][0][hl] + S.red[grp][1][hl]) + (S.red[grp][2][hl] + S.red[grp][3][hl]);
-      const float inv_l = total == 0.f ? 0.f : 1.f / total;
-      const int64_t row = p.splits == 1 ? static_cast<int64_t>(I.t) * p.H
-                                        : (static_cast<int64_t>(I.t) * p.splits + I.sp) * p.H;
-      if (quad == 0 && lane < kGH) {
-        const float lse = total == 0.f ? -INFINITY : (S.m[grp * kGH + lane] + log2f(total)) * 0.6931471805599453f;
-        S.m[grp * kGH + lane] = 0.f;                // for the next item
-        if (h0 + lane < p.H) {
-          if (p.splits > 1)
-            p.part_lse[row + h0 + lane] = lse;
-          else if (p.lse)
-            p.lse[row + h0 + lane] = lse;
-        }
-      }
-      bad |= !meet(&S.sync[grp], met, lane, p.status, ab);       // red may be reused, m is reset
-      if (tiles > 0) bad |= !wait(&S.o_full, (nq - 1) & 1, p.status, ab);
-      if ((bad = __any_sync(0xffffffffu, bad))) break;
-      if (p.splits > 1 && tiles == 0) continue;     // the combine skips parts of weight 0
-      tc_fence_after();
-      float iv[kGH];
-#pragma unroll
-      for (int i = 0; i < kGH; ++i) iv[i] = __shfl_sync(0xffffffffu, inv_l, i);
-      // Lanes hold neighbouring dims of every head: a pair of lanes trades, so that the even
-      // one has two dims of an even head and the odd one two dims of the odd head after it.
-      const int odd = lane & 1;
-#pragma unroll 1
-      for (int mt = 0; mt < 4; ++mt) {
-        uint32_t o[16];
-        if (tiles > 0) {
-          tmem_ld16(o_at + mt * kHT, o);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int i = 0; i < kGH; ++i) o[i] = 0;
-        }
-        const int64_t at0 = (row + h0 + odd) * DSA_D_V + mt * 128 + r - odd;
 #pragma unroll
         for (int i = 0; i < kGH; i += 2) {
-          const float a = __uint_as_float(o[i]) * iv[i], c = __uint_as_float(o[i + 1]) * iv[i + 1];
-          const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
-          const float d0 = odd ? got : a, d1 = odd ? c : got;
-          if (h0 + i < p.H) {                       // H is even
-            if (p.splits > 1) {
-              *reinterpret_cast<float2*>(p.part_o + at0 + i * DSA_D_V) = make_float2(d0, d1);
-            } else {
-              const __nv_bfloat162 y = __floats2bfloat162_rn(d0, d1);
-              *reinterpret_cast<uint32_t*>(p.out + at0 + i * DSA_D_V) = *reinterpret_cast<const uint32_t*>(&y);
-            }
-          }
+          const float2 y = ffma2(make_float2(x[i], x[i + 1]), make_float2(inv, inv), make_float2(l[i], l[i + 1]));
+          l[i] = y.x;
+          l[i + 1] = y.y;
         }
+        if (met_now) bad |= !meet(&S.sync[grp], met, lane, p.status, ab);   // m is set, red may be reused
       }
+      if ((bad = __any_sync(0xffffffffu, bad))) break;
       if (tiles > 0) {
-        tc_fence_before();
+        // the warp's part of the denominators, for the output warps
+        const float mine = reduce_transposed<false>(l, lane);
+        if (nq > 1) bad |= !wait(&S.l_free, nq & 1, p.status, ab);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.o_free);
+        if (lane < kGH) S.red[grp][quad][lane] = mine;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.l_full);
       }
+      if (it + step < p.items) next_queries(kk + 1, it + step);
     }
   } else if (warp < kSoftWarps + kGatherWarps) {
     // ================================================================ rows
-    setmaxnreg_dec<kGatherRegs>();
+    set_regs<kGatherRegs>();
     const int gw = warp - kSoftWarps, gt = tid - 32 * kSoftWarps;
     uint32_t g = 0, met = 0;
     bool bad = false;                               // a wait ran out
@@ -524,9 +532,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       if (!I.ok && gt == 0) set_status(p.status, DSA_DEV_BAD_QUERY);
       int tiles = I.e1 > I.e0 ? (I.e1 - I.e0 + kRows - 1) / kRows : 0;
       const int32_t* list = p.idx ? p.idx + static_cast<int64_t>(I.t) * p.k : nullptr;
-      // the lane's entries: lanes 0-15 rows 16 gw .. of the pair's first tile, 16-31 of its second
+      // The warp gathers four rows of each quarter of a tile.  The lane's entries: lanes
+      // 4 k + i row 32 k + 4 gw + i of the pair's first tile, lanes 16 + 4 k + i of its second.
+      const int my_row = ((lane & 15) >> 2) * 32 + gw * 4 + (lane & 3);
       auto entry = [&](int pair) {
-        const int e = I.e0 + (2 * pair + (lane >> 4)) * kRows + gw * 16 + (lane & 15);
+        const int e = I.e0 + (2 * pair + (lane >> 4)) * kRows + my_row;
         const int v = e < I.e1 ? (list ? __ldg(list + e) : e) : -1;
         return v < I.len ? v : -1;
       };
@@ -577,33 +587,36 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       }
       float sc = scale_of(row);
       int pg_nxt = page(v_nxt);
-      // tile by tile; the next pair's page, row and scale are looked up meanwhile
-      for (int j = 0; j < tiles; ++j, ++g) {
+      // a tile's rows; the next pair's page, row and scale are looked up meanwhile
+      auto gather = [&](int j) {
         if (!(sc >= 7.888609e-31f && sc <= 1.2676506e30f)) {   // 2^-100 .. 2^100
           if (row >= 0) set_status(p.status, DSA_DEV_BAD_SCALE);
           row = -1;
           sc = 0.f;
         }
         const int b = g & 1, half = j & 1;
-        bad |= g > 1 && !wait(&S.rows_empty[b][gw >> 1], ((g - 2) >> 1) & 1, p.status, ab);
-        if ((bad = __any_sync(0xffffffffu, bad))) break;
         const uint32_t lat = smem_u32(S.rows[b].lat[0]) + (lane >> 3) * (kRows * 128);
+        const uint32_t rope = smem_u32(S.rows[b].rope);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int rr = gw * 16 + i;
-          const int src = __shfl_sync(0xffffffffu, row, half * 16 + i);
-          cp_async16(lat + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4),
-                     p.kv8 + static_cast<int64_t>(max(src, 0)) * DSA_D_QK + lane * 16, src < 0 ? 0u : 16u);
-        }
+        for (int k = 0; k < 4; ++k) {
+          bad |= g > 1 && !wait(&S.rows_empty[b][k], ((g - 2) >> 1) & 1, p.status, ab);
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int rl = i * 8 + (lane >> 2), rr = gw * 16 + rl;
-          const int src = __shfl_sync(0xffffffffu, row, half * 16 + rl);
-          cp_async16(smem_u32(S.rows[b].rope) + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4),
-                     p.kv8 + static_cast<int64_t>(max(src, 0)) * DSA_D_QK + DSA_D_V + (lane & 3) * 16,
-                     src < 0 ? 0u : 16u);
+          for (int i = 0; i < 4; ++i) {
+            const int rr = k * 32 + gw * 4 + i;
+            const int src = __shfl_sync(0xffffffffu, row, half * 16 + k * 4 + i);
+            cp_async16(lat + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4),
+                       p.kv8 + static_cast<int64_t>(max(src, 0)) * DSA_D_QK + lane * 16, src < 0 ? 0u : 16u);
+          }
+          const int src = __shfl_sync(0xffffffffu, row, half * 16 + k * 4 + ((lane >> 2) & 3));
+          if (lane < 16) {
+            const int rr = k * 32 + gw * 4 + (lane >> 2);
+            cp_async16(rope + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4),
+                       p.kv8 + static_cast<int64_t>(max(src, 0)) * DSA_D_QK + DSA_D_V + (lane & 3) * 16,
+                       src < 0 ? 0u : 16u);
+          }
         }
-        if ((lane >> 4) == half) S.s_row[b][gw * 16 + (lane & 15)] = row < 0 ? 0.f : sc;
+        if ((lane >> 4) == half) S.s_row[b][my_row] = row < 0 ? 0.f : sc;
         cp_async_arrive_noinc(&S.rows_full[b]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.rows_full[b]);
@@ -613,17 +626,127 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
           v_nxt = entry((j >> 1) + 2);
           pg_nxt = page(v_nxt);
         }
+        ++g;
+      };
+      for (int j = 0; j < tiles; ++j) {
+        gather(j);
+        if ((bad = __any_sync(0xffffffffu, bad))) break;
       }
       bad = __any_sync(0xffffffffu, bad);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp < kSoftWarps + kGatherWarps + kOutWarps) {
+    // ================================================================ output
+    set_regs<kOutRegs>();
+    const int quad = warp & 3;                      // TMEM lanes 32 quad ..
+    const int r = quad * 32 + lane;
+    const uint32_t o_at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kOCol;
+    uint32_t nq = 0;
+    bool bad = false;
+    for (int kk = 0, it = blockIdx.x; it < p.items; ++kk, it += step) {
+      if (it + step < p.items) {                    // the next item's queries on their way to L2
+        Item N;
+        item_place(p, it + step, N);
+        const int lines = min(kHT, p.H - N.hg * kHT) * (DSA_D_QK * 2 / 128);
+        const char* src =
+            reinterpret_cast<const char*>(p.q + (static_cast<int64_t>(N.t) * p.H + N.hg * kHT) * DSA_D_QK);
+        for (int i = r; i < lines; i += 32 * kOutWarps)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i * 128));
+      }
+      bad |= !wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
+      const bool any = S.plan[kk & 1] > 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
+      Item I;
+      item_place(p, it, I);
+      const int h0 = I.hg * kHT;
+      const int64_t row = p.splits == 1 ? static_cast<int64_t>(I.t) * p.H
+                                        : (static_cast<int64_t>(I.t) * p.splits + I.sp) * p.H;
+      float inv[2];                                 // of heads lane and 32 + lane
+      if (any) bad |= !wait(&S.l_full, nq & 1, p.status, ab);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int h = 32 * u + lane;
+        float total = 0.f;
+        if (any) {
+          const float(&part)[4][kGH] = S.red[h / kGH];
+          const int i = h % kGH;
+          total = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+        }
+        inv[u] = total == 0.f ? 0.f : 0.00390625f / total;       // O holds 2^8 times the weights
+        if (quad == 0 && h0 + h < p.H) {
+          const float lse = total == 0.f ? -INFINITY : (log2f(total) - S.m[h]) * 0.6931471805599453f;
+          if (p.splits > 1)
+            p.part_lse[row + h0 + h] = lse;
+          else if (p.lse)
+            p.lse[row + h0 + h] = lse;
+        }
+      }
+      if (any) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.l_free);
+        bad |= !wait(&S.o_full, nq & 1, p.status, ab);
+        ++nq;
+      }
+      if ((bad = __any_sync(0xffffffffu, bad))) break;
+      if (!any && p.splits > 1) continue;           // the combine skips parts of weight 0
+      tc_fence_after();
+      // Lanes hold neighbouring dims of every head.  A pair of lanes trades, so that the even
+      // one has two dims of an even head and the odd one two dims of the odd head after it.
+      const int odd = lane & 1;
+      const int64_t at0 = (row + h0 + odd) * DSA_D_V + r - odd;
+#pragma unroll 1
+      for (int hc = 0; hc < kHT; hc += 16) {
+        float iv[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) iv[i] = __shfl_sync(0xffffffffu, hc < 32 ? inv[0] : inv[1], (hc + i) & 31);
+        const int heads = p.H - h0 - hc;
+#pragma unroll 1
+        for (int mt = 0; mt < 4; ++mt) {
+          uint32_t o[16];
+          if (any) {
+            tmem_ld16(o_at + mt * kHT + hc, o);
+            tmem_ld_wait();
+            if (hc == kHT - 16 && mt == 3) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&S.o_free);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = 0;
+          }
+          const int64_t at = at0 + mt * 128 + hc * DSA_D_V;
+          if (p.splits > 1) {
+            float* dst = p.part_o + at;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float2 y = mul2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                                    make_float2(iv[i], iv[i + 1]));
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.y, 1);
+              if (i < heads)                        // H is even
+                *reinterpret_cast<float2*>(dst + i * DSA_D_V) = make_float2(odd ? got : y.x, odd ? y.y : got);
+            }
+          } else {
+            uint16_t* dst = p.out + at;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float2 y = mul2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                                    make_float2(iv[i], iv[i + 1]));
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.y, 1);
+              const __nv_bfloat162 z = __floats2bfloat162_rn(odd ? got : y.x, odd ? y.y : got);
+              if (i < heads) *reinterpret_cast<uint32_t*>(dst + i * DSA_D_V) = *reinterpret_cast<const uint32_t*>(&z);
+            }
+          }
+        }
+      }
+    }
   } else {
-    setmaxnreg_dec<kIssueRegs>();
-    if (warp == kSoftWarps + kGatherWarps && lane == 0) {
+    set_regs<kIssueRegs>();
+    if (warp == kSoftWarps + kGatherWarps + kOutWarps && lane == 0) {
       // ================================================================ S^T = codes . Q^T
       const uint32_t id = instr_desc(0, 0, false, false, 128, 2 * kHT);
-      const uint64_t q_lat = smem_desc_sw128(smem_u32(S.q.lat[0]), 16, 1024);
-      const uint64_t q_rope = smem_desc_sw64(smem_u32(S.q.rope), 512);
+      const uint32_t q_lat = desc_lo(S.q.lat[0]), q_rope = desc_lo(S.q.rope);
       uint32_t g = 0, nq = 0;
       bool ok = true;
       for (int kk = 0, it = blockIdx.x; it < p.items && ok; ++kk, it += step) {
@@ -642,17 +765,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
           }
           fence_proxy_async_smem();                 // cp.async writes -> tensor-core reads
           tc_fence_after();
-          const uint64_t a_lat = smem_desc_sw128(smem_u32(S.rows[b].lat[0]), 16, 1024);
-          const uint64_t a_rope = smem_desc_sw64(smem_u32(S.rows[b].rope), 512);
+          const uint32_t a_lat = desc_lo(S.rows[b].lat[0]), a_rope = desc_lo(S.rows[b].rope);
           const uint32_t d = tmem + kSCol + b * 128;
+#pragma unroll 1
+          for (uint32_t c = 0; c < 4 * (kRows * 128 / 16); c += kRows * 128 / 16)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (uint32_t k = 0; k < 8; k += 2) mma<kDesc128, kDesc128>(d, a_lat + c + k, q_lat + c + k, id, (c | k) != 0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f8(d, a_lat + c * (kRows * 128 / 16) + k * 2, q_lat + c * (kRows * 128 / 16) + k * 2, id,
-                      (c | k) != 0 ? 1u : 0u);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) umma_f8(d, a_rope + k * 2, q_rope + k * 2, id, 1u);
+          for (uint32_t k = 0; k < 4; k += 2) mma<kDesc64, kDesc64>(d, a_rope + k, q_rope + k, id, true);
           umma_commit(&S.s_full[b]);
         }
         if (!ok) break;
@@ -660,10 +780,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       }
       umma_commit(&S.done);
       mbar_wait(&S.done, 0, p.status, nullptr);
-    } else if (warp == kSoftWarps + kGatherWarps + 1 && lane == 0) {
+    } else if (warp == kSoftWarps + kGatherWarps + kOutWarps + 1 && lane == 0) {
       // ================================================================ O^T += codes^T . W
       const uint32_t id = instr_desc(0, 0, true, true, 128, kHT);
-      const uint64_t w_lo = smem_desc_sw64(smem_u32(S.w_lo), 512);
+      const uint32_t w_lo = desc_lo(S.w_lo);
       uint32_t g = 0, no = 0;
       bool ok = true;
       for (int kk = 0, it = blockIdx.x; it < p.items && ok; ++kk, it += step) {
@@ -675,8 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         ++no;
         for (int j = 0; j < tiles && ok; ++j, ++g) {
           const int b = g & 1;
-          const uint64_t a = smem_desc_sw128(smem_u32(S.rows[b].lat[0]), 16, 1024);
-          const uint64_t w_hi = smem_desc_sw64(smem_u32(S.rows[b].rope), 512);
+          const uint32_t a = desc_lo(S.rows[b].lat[0]), w_hi = desc_lo(S.rows[b].rope);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (!wait(&S.w_full[k], g & 1, p.status, ab)) {
@@ -686,9 +805,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
             tc_fence_after();
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-              const uint64_t am = a + mt * (kRows * 128 / 16) + k * (32 * 128 / 16);
-              umma_f8(tmem + kOCol + mt * kHT, am, w_lo + k * (32 * 64 / 16), id, (j | k) != 0 ? 1u : 0u);
-              umma_f8(tmem + kOCol + mt * kHT, am, w_hi + k * (32 * 64 / 16), id, 1u);
+              const uint32_t am = a + mt * (kRows * 128 / 16) + k * (32 * 128 / 16), wk = k * (32 * 64 / 16);
+              mma<kDesc128, kDesc64>(tmem + kOCol + mt * kHT, am, w_lo + wk, id, (j | k) != 0);
+              mma<kDesc128, kDesc64>(tmem + kOCol + mt * kHT, am, w_hi + wk, id, true);
             }
             umma_commit(&S.rows_empty[b][k]);
           }
@@ -703,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kSoftWarps + kGatherWarps) {
+  if (warp == kSoftWarps + kGatherWarps + kOutWarps) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
