@@ -27,7 +27,9 @@
 // its rows and weights back, so the next tile's rows and weights follow it closely.
 // 32 warps: 0-15 softmax (warp w: rows 32 (w mod 4) .., 16 heads) and, between items,
 // the next queries' hi/lo split, 16-23 row gathers (16-byte cp.async), 24-27 the
-// output (while the softmax is at the next item), 28 issues S^T, 29 O^T.  Registers:
+// output (while the softmax is at the next item), 28 issues S^T, 29 O^T (as whole warps,
+// so that the descriptors are worked out in uniform registers; a lone lane's cost
+// some 100 clocks a product to issue).  Registers:
 // launched at 64 per thread, softmax 80, gathers 56, output 48, issuers 32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -69,7 +71,7 @@ struct Q8Smem {
   uint8_t w_lo[kRows * 64];
   float s_row[2][kRows];                           // row scales, 0 = unused row
   float red[kGroups][4][kGH];
-  uint16_t qs[2][kHT];                             // 2^-e of each head's query, bf16
+  float qs[kHT];                                   // scale of each head's query
   float m[kHT];                                    // minus the references
   uint64_t rows_full[2], rows_empty[2][4], s_full[2], s_free[2], w_full[4], q_full, q_free, o_full, o_free, l_full, l_free,
       plan_full[2], plan_free[2], vote[kGroups], sync[kGroups], gather_sync, done;
@@ -118,8 +120,8 @@ __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
 // taken off, E4M3's exponent field equals fp16's low four exponent bits, its
 // subnormals start where fp16's do, and a code is bits 7 .. 14 of the fp16 pattern
 // (bit 14 is 0 below 2).  So hi is the pattern cut after 3 mantissa bits, lo the
-// exact rest rounded to 3, and both come from integer operations (the E4M3
-// conversion instructions run at a sixteenth of their rate).  NaN stays NaN in hi.
+// exact rest rounded to 3, and both come from integer operations (measured 64 lanes
+// a clock and SM; the E4M3 conversions 32, and more of them).  NaN stays NaN in hi.
 template <bool kSigned>
 __device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
   uint32_t x0, x1, r0, r1;
@@ -173,6 +175,12 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {   // one ulp; exact for powers of two
@@ -240,8 +248,9 @@ __device__ __forceinline__ void item_list(const MlaQ8Params& p, Item& I) {
 
 // Splits the 64 heads' queries of an item into hi and lo (this warp: heads w0 + 16 i) and
 // stores them as the first product's operand.  A lane takes 4 neighbouring entries
-// of each 128 (and lanes 0-15 4 of the last 64).
-__device__ __forceinline__ void split_queries(const MlaQ8Params& p, Q8Smem& S, int t, int hg, uint32_t slot, int w0,
+// of each 128 (and lanes 0-15 4 of the last 64).  The item is the ord-th with rows; the
+// first product is through with the queries of the one before.
+__device__ __forceinline__ bool split_queries(const MlaQ8Params& p, Q8Smem& S, int t, int hg, uint32_t ord, int w0,
                                               int lane) {
   const uint2* src0 =
       reinterpret_cast<const uint2*>(p.q + (static_cast<int64_t>(t) * p.H + hg * kHT) * DSA_D_QK) + lane;
@@ -252,7 +261,7 @@ __device__ __forceinline__ void split_queries(const MlaQ8Params& p, Q8Smem& S, i
     for (int i = 0; i < 5; ++i)
       v[i] = hl < heads && (i < 4 || lane < 16) ? __ldg(src + i * 32) : make_uint2(0u, 0u);
   };
-  auto split = [&](int hl, const uint2(&v)[5]) {
+  auto split = [&](int hl, const uint2(&v)[5]) -> float {
     uint32_t am = 0;                                // two 16-bit maxima
 #pragma unroll
     for (int i = 0; i < 5; ++i) am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu));
@@ -261,7 +270,6 @@ __device__ __forceinline__ void split_queries(const MlaQ8Params& p, Q8Smem& S, i
     int e = 126 - static_cast<int>(am >> 7);
     if (e > 118) e = 118;
     const float up = __uint_as_float(e >= -126 ? static_cast<uint32_t>(e + 127) << 23 : 0x00800000u >> (-126 - e));
-    if (lane == 0) S.qs[slot][hl] = static_cast<uint16_t>((119 - e) << 7);   // 2^-(e + 8)
     const bool bad = am >= 0x7f80u;                 // an infinity or NaN: the head's results are NaN
     uint8_t* lat = &S.q.lat[0][hl * 128 + ((lane >> 2) ^ (hl & 7)) * 16 + (lane & 3) * 4];
     uint8_t* rope = &S.q.rope[hl * 64 + (((lane >> 2) & 3) ^ ((hl >> 1) & 3)) * 16 + (lane & 3) * 4];
@@ -282,22 +290,34 @@ __device__ __forceinline__ void split_queries(const MlaQ8Params& p, Q8Smem& S, i
         *reinterpret_cast<uint32_t*>(rope + kHT * 64) = lo;
       }
     }
+    return __uint_as_float(static_cast<uint32_t>(119 - e) << 23);   // 2^-(e + 8)
   };
   constexpr int kPer = kHT / kSoftWarps;
-  uint2 w[kPer][5];                                 // all loads in flight
+  float qs = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < kPer; i += 2) {
+    uint2 w[2][5];                                  // the loads of two heads in flight
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) load(w0 + i * kSoftWarps, w[i]);
+    for (int u = 0; u < 2; ++u) load(w0 + (i + u) * kSoftWarps, w[u]);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) split(w0 + i * kSoftWarps, w[i]);
+    for (int u = 0; u < 2; ++u) {
+      const float q = split(w0 + (i + u) * kSoftWarps, w[u]);
+      if (lane == i + u) qs = q;
+    }
+  }
   fence_proxy_async_smem();
+  // every warp is through with the last item's logits, which read its scales
+  const bool ok = ord == 0 || wait(&S.l_full, (ord - 1) & 1, p.status, &S.abort);
+  if (lane < kPer) S.qs[w0 + lane * kSoftWarps] = qs;
   __syncwarp();
   if (lane == 0) mbar_arrive(&S.q_full);
+  return ok;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
   extern __shared__ __align__(1024) uint8_t raw[];
   Q8Smem& S = *reinterpret_cast<Q8Smem*>(raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   volatile int* ab = &S.abort;
   if (tid == 0) {
     S.abort = 0;
@@ -333,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = S.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, S.tmem, 0);
   const int step = gridDim.x;
 
   if (warp < kSoftWarps) {
@@ -346,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     const float c0 = p.sm_scale * 1.4426950408889634f;
     uint32_t g = 0, nq = 0, met = 0, votes = 0;     // tiles, non-empty items, meetings, votes so far
     bool bad = false;                               // a wait ran out
-    int tiles_next = 0, tiles_last = 0;             // tiles of the next item, of the last non-empty one
+    int tiles_next = 0;                             // tiles of the next item
     // the tiles of the kk-th item, and its queries' operand if it has any
     auto next_queries = [&](int kk, int it) {
       bad |= !wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
@@ -356,18 +376,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       if (tiles_next == 0) return;
       // the products of the last item have read its queries
       bad |= nq > 0 && !wait(&S.q_free, (nq - 1) & 1, p.status, ab);
-      // qs has two places: every warp must be through with the logits of the item before the
-      // last one (it is, unless the last one's only tile may have run ahead)
-      if (tiles_last == 1 && g > 1) bad |= !wait(&S.s_free[g & 1], ((g - 2) >> 1) & 1, p.status, ab);
       __syncwarp();
       Item I;
       item_place(p, it, I);
-      split_queries(p, S, I.t, I.hg, nq & 1, warp, lane);
+      bad |= !split_queries(p, S, I.t, I.hg, nq, warp, lane);
     };
     if (blockIdx.x < p.items) next_queries(0, blockIdx.x);
     for (int kk = 0, it = blockIdx.x; it < p.items; ++kk, it += step) {
       const int tiles = tiles_next;
-      const uint32_t slot = nq & 1;
       float l[kGH];
 #pragma unroll
       for (int i = 0; i < kGH; ++i) l[i] = 0.f;
@@ -375,7 +391,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       if (tiles > 0) {
         bad |= !wait(&S.q_full, nq & 1, p.status, ab);
         ++nq;
-        tiles_last = tiles;
       }
       for (int j = 0; j < tiles; ++j, ++g) {
         const int b = g & 1;
@@ -391,22 +406,28 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         uint32_t wh[4], wl[4];
         float x[kGH];                               // log2 of the weight, then the weight
         auto logits = [&]() {
-          uint32_t hi[kGH], lo[kGH];
-          tmem_ld16(s_at + b * 128, hi);
-          tmem_ld16(s_at + b * 128 + kHT, lo);
+          uint32_t hi[2][8], lo[2][8];
+          tmem_ld8(s_at + b * 128, hi[0]);
+          tmem_ld8(s_at + b * 128 + kHT, lo[0]);
           tmem_ld_wait();
+          tmem_ld8(s_at + b * 128 + 8, hi[1]);
+          tmem_ld8(s_at + b * 128 + kHT + 8, lo[1]);
 #pragma unroll
-          for (int i = 0; i < kGH; i += 2) {
-            const uint32_t sc = *reinterpret_cast<const uint32_t*>(&S.qs[slot][grp * kGH + i]);
-            const float2 mm = *reinterpret_cast<const float2*>(&S.m[grp * kGH + i]);
-            const float2 d = add2(make_float2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
-                                  make_float2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
-            const float2 k = mul2(make_float2(__uint_as_float(sc << 16), __uint_as_float(sc & 0xffff0000u)),
-                                  make_float2(c, c));
-            // an item's first logits have no reference yet
-            const float2 y = ffma2(d, k, seen ? add2(make_float2(sg, sg), mm) : make_float2(sg, sg));
-            x[i] = y.x;
-            x[i + 1] = y.y;
+          for (int u = 0; u < 2; ++u) {
+            if (u == 1) tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const int h = u * 8 + i;
+              const float2 sc = *reinterpret_cast<const float2*>(&S.qs[grp * kGH + h]);
+              const float2 mm = *reinterpret_cast<const float2*>(&S.m[grp * kGH + h]);
+              const float2 d = add2(make_float2(__uint_as_float(hi[u][i]), __uint_as_float(hi[u][i + 1])),
+                                    make_float2(__uint_as_float(lo[u][i]), __uint_as_float(lo[u][i + 1])));
+              // an item's first logits have no reference yet
+              const float2 y = ffma2(d, mul2(sc, make_float2(c, c)),
+                                     seen ? add2(make_float2(sg, sg), mm) : make_float2(sg, sg));
+              x[h] = y.x;
+              x[h + 1] = y.y;
+            }
           }
         };
         logits();
@@ -414,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
 #pragma unroll
           for (int i = 0; i < kGH; ++i) x[i] = ex2_approx(x[i]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) split4<false>(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], wh[i], wl[i]);
+          for (int i = 0; i < kGH / 4; ++i) split4<false>(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], wh[i], wl[i]);
         };
         // The largest logit over the group's 128 rows, of head 16 grp + lane mod 16 (of NaN
         // only: -infinity).  red and m may still hold the last item's sums and references.
@@ -483,10 +504,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
               if (lane < kGH) S.m[grp * kGH + lane] -= up;
               if (lane == 0) S.over[grp][votes & 1] = 0;
             }
-#pragma unroll
-            for (int i = 0; i < kGH; ++i) x[i] -= __shfl_sync(0xffffffffu, up, i);
+            bad |= !meet(&S.sync[grp], met, lane, p.status, ab);   // m is set, red may be reused
+            logits();
             weights();
-            met_now = true;
           }
           ++votes;
         }
@@ -743,80 +763,85 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     }
   } else {
     set_regs<kIssueRegs>();
-    if (warp == kSoftWarps + kGatherWarps + kOutWarps && lane == 0) {
+    constexpr uint32_t kChunk = kRows * 128 / 16;   // a tile's 128-dim chunk, in descriptor units
+    constexpr uint32_t kTile = sizeof(Tile) / 16;
+    static_assert(offsetof(Q8Smem, rows) == sizeof(Tile) && offsetof(Q8Smem, w_lo) == 3 * sizeof(Tile), "");
+    const uint32_t q0 = __shfl_sync(0xffffffffu, desc_lo(S.q.lat[0]), 0);   // then the row tiles, then W_lo
+    uint32_t g = 0, n = 0;                          // tiles, items with rows so far
+    bool ok = true;
+    if (warp == kSoftWarps + kGatherWarps + kOutWarps) {
       // ================================================================ S^T = codes . Q^T
-      const uint32_t id = instr_desc(0, 0, false, false, 128, 2 * kHT);
-      const uint32_t q_lat = desc_lo(S.q.lat[0]), q_rope = desc_lo(S.q.rope);
-      uint32_t g = 0, nq = 0;
-      bool ok = true;
+      constexpr uint32_t id = instr_desc(0, 0, false, false, 128, 2 * kHT);
       for (int kk = 0, it = blockIdx.x; it < p.items && ok; ++kk, it += step) {
-        if (!wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab)) break;
-        const int tiles = S.plan[kk & 1];
-        mbar_arrive(&S.plan_free[kk & 1]);
+        ok = wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
+        const int tiles = __shfl_sync(0xffffffffu, S.plan[kk & 1], 0);
+        if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
+        if (tiles > 0) ok = ok && wait(&S.q_full, n & 1, p.status, ab);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         if (tiles == 0) continue;
-        if (!wait(&S.q_full, nq & 1, p.status, ab)) break;
-        ++nq;
+        ++n;
         for (int j = 0; j < tiles; ++j, ++g) {
-          const int b = g & 1;
-          const uint32_t ph = (g >> 1) & 1;
-          if ((g > 1 && !wait(&S.s_free[b], ph ^ 1, p.status, ab)) || !wait(&S.rows_full[b], ph, p.status, ab)) {
-            ok = false;
-            break;
-          }
-          fence_proxy_async_smem();                 // cp.async writes -> tensor-core reads
-          tc_fence_after();
-          const uint32_t a_lat = desc_lo(S.rows[b].lat[0]), a_rope = desc_lo(S.rows[b].rope);
-          const uint32_t d = tmem + kSCol + b * 128;
-#pragma unroll 1
-          for (uint32_t c = 0; c < 4 * (kRows * 128 / 16); c += kRows * 128 / 16)
-#pragma unroll
-            for (uint32_t k = 0; k < 8; k += 2) mma<kDesc128, kDesc128>(d, a_lat + c + k, q_lat + c + k, id, (c | k) != 0);
-#pragma unroll
-          for (uint32_t k = 0; k < 4; k += 2) mma<kDesc64, kDesc64>(d, a_rope + k, q_rope + k, id, true);
-          umma_commit(&S.s_full[b]);
-        }
-        if (!ok) break;
-        umma_commit(&S.q_free);
-      }
-      umma_commit(&S.done);
-      mbar_wait(&S.done, 0, p.status, nullptr);
-    } else if (warp == kSoftWarps + kGatherWarps + kOutWarps + 1 && lane == 0) {
-      // ================================================================ O^T += codes^T . W
-      const uint32_t id = instr_desc(0, 0, true, true, 128, kHT);
-      const uint32_t w_lo = desc_lo(S.w_lo);
-      uint32_t g = 0, no = 0;
-      bool ok = true;
-      for (int kk = 0, it = blockIdx.x; it < p.items && ok; ++kk, it += step) {
-        if (!wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab)) break;
-        const int tiles = S.plan[kk & 1];
-        mbar_arrive(&S.plan_free[kk & 1]);
-        if (tiles == 0) continue;
-        if (no > 0 && !wait(&S.o_free, (no - 1) & 1, p.status, ab)) break;
-        ++no;
-        for (int j = 0; j < tiles && ok; ++j, ++g) {
-          const int b = g & 1;
-          const uint32_t a = desc_lo(S.rows[b].lat[0]), w_hi = desc_lo(S.rows[b].rope);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (!wait(&S.w_full[k], g & 1, p.status, ab)) {
-              ok = false;
-              break;
-            }
+          const uint32_t b = g & 1, ph = (g >> 1) & 1;
+          ok = (g <= 1 || wait(&S.s_free[b], ph ^ 1, p.status, ab)) && wait(&S.rows_full[b], ph, p.status, ab);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          const uint32_t a = q0 + kTile + b * kTile, d = tmem + kSCol + b * 128;
+          if (elect_one_sync()) {
+            fence_proxy_async_smem();               // cp.async writes -> tensor-core reads
             tc_fence_after();
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-              const uint32_t am = a + mt * (kRows * 128 / 16) + k * (32 * 128 / 16), wk = k * (32 * 64 / 16);
-              mma<kDesc128, kDesc64>(tmem + kOCol + mt * kHT, am, w_lo + wk, id, (j | k) != 0);
-              mma<kDesc128, kDesc64>(tmem + kOCol + mt * kHT, am, w_hi + wk, id, true);
+            for (uint32_t c = 0; c < 4 * kChunk; c += kChunk)
+#pragma unroll
+              for (uint32_t s = 0; s < 8; s += 2) mma<kDesc128, kDesc128>(d, a + c + s, q0 + c + s, id, (c | s) != 0);
+#pragma unroll
+            for (uint32_t s = 0; s < 4; s += 2)
+              mma<kDesc64, kDesc64>(d, a + 4 * kChunk + s, q0 + 4 * kChunk + s, id, true);
+            umma_commit(&S.s_full[b]);
+            if (j == tiles - 1) umma_commit(&S.q_free);
+          }
+          __syncwarp();
+        }
+      }
+      if (elect_one_sync()) {
+        umma_commit(&S.done);
+        mbar_wait(&S.done, 0, p.status, nullptr);
+      }
+    } else if (warp == kSoftWarps + kGatherWarps + kOutWarps + 1) {
+      // ================================================================ O^T += codes^T . W
+      constexpr uint32_t id = instr_desc(0, 0, true, true, 128, kHT);
+      for (int kk = 0, it = blockIdx.x; it < p.items && ok; ++kk, it += step) {
+        ok = wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
+        const int tiles = __shfl_sync(0xffffffffu, S.plan[kk & 1], 0);
+        if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
+        if (tiles > 0 && n > 0) ok = ok && wait(&S.o_free, (n - 1) & 1, p.status, ab);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (tiles == 0) continue;
+        ++n;
+        for (int j = 0; j < tiles && ok; ++j, ++g) {
+          const uint32_t b = g & 1;
+          const uint32_t a = q0 + kTile + b * kTile;
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k) {
+            if (!(ok = __all_sync(0xffffffffu, ok && wait(&S.w_full[k], g & 1, p.status, ab)))) break;
+            if (elect_one_sync()) {
+              tc_fence_after();
+              const uint32_t wk = k * (32 * 64 / 16);
+#pragma unroll
+              for (uint32_t mt = 0; mt < 4; ++mt) {
+                const uint32_t am = a + mt * kChunk + k * (32 * 128 / 16);
+                mma<kDesc128, kDesc64>(tmem + kOCol + mt * kHT, am, q0 + 3 * kTile + wk, id, j > 0 || k > 0);
+                mma<kDesc128, kDesc64>(tmem + kOCol + mt * kHT, am, a + 4 * kChunk + wk, id, true);
+              }
+              umma_commit(&S.rows_empty[b][k]);
+              if (k == 3 && j == tiles - 1) umma_commit(&S.o_full);
             }
-            umma_commit(&S.rows_empty[b][k]);
+            __syncwarp();
           }
         }
-        if (!ok) break;
-        umma_commit(&S.o_full);
       }
-      umma_commit(&S.done);
-      mbar_wait(&S.done, 0, p.status, nullptr);
+      if (elect_one_sync()) {
+        umma_commit(&S.done);
+        mbar_wait(&S.done, 0, p.status, nullptr);
+      }
     }
   }
   __syncwarp();
