@@ -115,13 +115,20 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// 2 x + c on the multiply pipe: the integer pipe (64 lanes a clock and SM, as are the
+// fp16 packing and half of it the E4M3 conversions) is what the softmax runs short of.
+__device__ __forceinline__ uint32_t twice_plus(uint32_t x, uint32_t c) {
+  uint32_t y;
+  asm("mad.lo.u32 %0, %1, 2, %2;" : "=r"(y) : "r"(x), "r"(c));
+  return y;
+}
+
 // Four fp32 values of magnitude below 2 -> E4M3 codes of hi and lo, hi + lo = 2^8 times
 // the value to 8 significant bits (byte i = value i).  By way of fp16: with the 2^8
 // taken off, E4M3's exponent field equals fp16's low four exponent bits, its
 // subnormals start where fp16's do, and a code is bits 7 .. 14 of the fp16 pattern
 // (bit 14 is 0 below 2).  So hi is the pattern cut after 3 mantissa bits, lo the
-// exact rest rounded to 3, and both come from integer operations (measured 64 lanes
-// a clock and SM; the E4M3 conversions 32, and more of them).  NaN stays NaN in hi.
+// exact rest rounded to 3.  NaN stays NaN in hi.
 template <bool kSigned>
 __device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
   uint32_t x0, x1, r0, r1;
@@ -129,10 +136,9 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x1) : "f"(d), "f"(c));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(x0), "r"(x0 & 0xff80ff80u));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(x1), "r"(x1 & 0xff80ff80u));
-  r0 += 0x00400040u;
-  r1 += 0x00400040u;
-  uint32_t h0 = x0 << 1, h1 = x1 << 1, l0 = r0 << 1, l1 = r1 << 1;
-  if (kSigned) {
+  uint32_t h0 = twice_plus(x0, 0), h1 = twice_plus(x1, 0);
+  uint32_t l0 = twice_plus(r0, 0x00800080u), l1 = twice_plus(r1, 0x00800080u);
+  if (kSigned) {                                    // the doubling moved the signs out
     h0 |= x0 & 0x80008000u;
     h1 |= x1 & 0x80008000u;
     l0 |= r0 & 0x80008000u;
@@ -140,6 +146,12 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
   }
   hi = __byte_perm(h0, h1, 0x7531);
   lo = __byte_perm(l0, l1, 0x7531);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 
 // Bounded wait that gives up at once when a thread of the CTA has given up.  Warps
@@ -466,7 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         } else {
           float top = x[0];
 #pragma unroll
-          for (int i = 1; i < kGH; ++i) top = fmaxf(top, x[i]);
+          for (int i = 1; i < kGH - 1; i += 2) top = max3(top, x[i], x[i + 1]);
+          top = fmaxf(top, x[kGH - 1]);
           // the group's vote on moving the reference; the weights are worked out meanwhile
           const bool over = __any_sync(0xffffffffu, top > kLimit);
           if (lane == 0) {
@@ -711,52 +724,64 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       if ((bad = __any_sync(0xffffffffu, bad))) break;
       if (!any && p.splits > 1) continue;           // the combine skips parts of weight 0
       tc_fence_after();
-      // Lanes hold neighbouring dims of every head.  A pair of lanes trades, so that the even
-      // one has two dims of an even head and the odd one two dims of the odd head after it.
+      // Lanes hold neighbouring dims of every head.  For bf16 a pair of lanes trades, so that
+      // the even one has two dims of an even head and the odd one two dims of the odd head
+      // after it.  The next columns are read from TMEM meanwhile.
       const int odd = lane & 1;
-      const int64_t at0 = (row + h0 + odd) * DSA_D_V + r - odd;
-#pragma unroll 1
-      for (int hc = 0; hc < kHT; hc += 16) {
-        float iv[16];
+      const uint32_t sel = odd ? 0x3276u : 0x5410u;
+      float* part = p.part_o + row * DSA_D_V + h0 * DSA_D_V + r;
+      uint16_t* out = p.out + (row + h0 + odd) * DSA_D_V + r - odd;
+      uint32_t o[2][8];
+      if (any) {
+        tmem_ld8(o_at, o[0]);
+      } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) iv[i] = __shfl_sync(0xffffffffu, hc < 32 ? inv[0] : inv[1], (hc + i) & 31);
-        const int heads = p.H - h0 - hc;
+        for (int i = 0; i < 8; ++i) o[0][i] = o[1][i] = 0;
+      }
 #pragma unroll 1
+      for (int hc = 0; hc < kHT; hc += 8) {         // 8 heads, then the four groups of 128 dims
+        float iv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) iv[i] = __shfl_sync(0xffffffffu, hc < 32 ? inv[0] : inv[1], (hc + i) & 31);
+        const int heads = p.H - h0 - hc;            // H is a multiple of 8: all of them or none
+#pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-          uint32_t o[16];
           if (any) {
-            tmem_ld16(o_at + mt * kHT + hc, o);
             tmem_ld_wait();
-            if (hc == kHT - 16 && mt == 3) {
+            if (mt < 3) {
+              tmem_ld8(o_at + hc + (mt + 1) * kHT, o[(mt + 1) & 1]);
+            } else if (hc + 8 < kHT) {
+              tmem_ld8(o_at + hc + 8, o[0]);
+            } else {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&S.o_free);
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = 0;
           }
-          const int64_t at = at0 + mt * 128 + hc * DSA_D_V;
-          if (p.splits > 1) {
-            float* dst = p.part_o + at;
+          if (heads <= 0) continue;
+          float2 y[4];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float2 y = mul2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
-                                    make_float2(iv[i], iv[i + 1]));
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.y, 1);
-              if (i < heads)                        // H is even
-                *reinterpret_cast<float2*>(dst + i * DSA_D_V) = make_float2(odd ? got : y.x, odd ? y.y : got);
+          for (int i = 0; i < 4; ++i)
+            y[i] = mul2(make_float2(__uint_as_float(o[mt & 1][2 * i]), __uint_as_float(o[mt & 1][2 * i + 1])),
+                        make_float2(iv[2 * i], iv[2 * i + 1]));
+          if (p.splits > 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              part[(hc + 2 * i) * DSA_D_V + mt * 128] = y[i].x;
+              part[(hc + 2 * i + 1) * DSA_D_V + mt * 128] = y[i].y;
             }
           } else {
-            uint16_t* dst = p.out + at;
+            uint32_t z[4], got[4];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float2 y = mul2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
-                                    make_float2(iv[i], iv[i + 1]));
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.y, 1);
-              const __nv_bfloat162 z = __floats2bfloat162_rn(odd ? got : y.x, odd ? y.y : got);
-              if (i < heads) *reinterpret_cast<uint32_t*>(dst + i * DSA_D_V) = *reinterpret_cast<const uint32_t*>(&z);
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 z2 = __floats2bfloat162_rn(y[i].x, y[i].y);
+              z[i] = *reinterpret_cast<const uint32_t*>(&z2);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) got[i] = __shfl_xor_sync(0xffffffffu, z[i], 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint32_t*>(out + (hc + 2 * i) * DSA_D_V + mt * 128) = __byte_perm(z[i], got[i], sel);
           }
         }
       }
