@@ -131,9 +131,19 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return t.data_ptr()
 
 
+def _dev(t: torch.Tensor | None, device: int) -> int | None:
+    """Pointer of a tensor that has to lie on the current device (whose stream the call takes)."""
+    if t is None:
+        return None
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError("tensors passed to the DSA library must be contiguous and on the current CUDA device")
+    return t.data_ptr()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: building a Stream object costs more than a small kernel
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -234,7 +244,7 @@ class PageBuffers:
             n = t.numel() * t.element_size()
             if n % num_pages:
                 raise ValueError("a page buffer holds a whole number of bytes per page")
-            self.struct.base[j] = _ptr(t)
+            self.struct.base[j] = _dev(t, t.get_device())
             self.struct.page_bytes[j] = n // num_pages
 
 
@@ -346,31 +356,35 @@ def dsa_forward(batch: DeviceBatch, q_idx, k_idx, w, H_I: int, q, kv, H: int, k:
 
 
 def dsa_quantize_append(batch: DeviceBatch, kv, kv8, scale, scale_block: int, ws, stream=None):
+    d = torch.cuda.current_device()
     _check("dsa_quantize_append", lib().dsa_quantize_append(
-        ctypes.byref(batch.struct), _ptr(kv), _ptr(kv8), _ptr(scale), scale_block, _ptr(ws), ws.numel(),
+        ctypes.byref(batch.struct), _dev(kv, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(ws, d), ws.numel(),
         _stream(stream)))
 
 
 def dsa_project_append_q8(batch: DeviceBatch, hidden, w_all, d_model: int, H_I: int, H: int, rope_base: float, q_idx,
                           w, q, k_idx, kv8, scale, scale_block: int, ws, stream=None):
+    d = torch.cuda.current_device()
     _check("dsa_project_append_q8", lib().dsa_project_append_q8(
-        ctypes.byref(batch.struct), _ptr(hidden), _ptr(w_all), d_model, H_I, H, rope_base, _ptr(q_idx), _ptr(w),
-        _ptr(q), _ptr(k_idx), _ptr(kv8), _ptr(scale), scale_block, _ptr(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(batch.struct), _dev(hidden, d), _dev(w_all, d), d_model, H_I, H, rope_base, _dev(q_idx, d), _dev(w, d),
+        _dev(q, d), _dev(k_idx, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(ws, d), ws.numel(), _stream(stream)))
 
 
 def dsa_sparse_mla_q8(batch: DeviceBatch, q, kv8, scale, scale_block: int, idx, k: int, H: int, sm_scale: float, out,
                       lse, ws, stream=None):
     """Attention over the 8-bit cache; idx = None with k = 0 attends to every visible key."""
+    d = torch.cuda.current_device()
     _check("dsa_sparse_mla_q8", lib().dsa_sparse_mla_q8(
-        ctypes.byref(batch.struct), _ptr(q), _ptr(kv8), _ptr(scale), scale_block, _ptr(idx), k, H, sm_scale,
-        _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(batch.struct), _dev(q, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(idx, d), k, H, sm_scale,
+        _dev(out, d), _dev(lse, d), _dev(ws, d), ws.numel(), _stream(stream)))
 
 
 def dsa_forward_q8(batch: DeviceBatch, q_idx, k_idx, w, H_I: int, q, kv8, scale, scale_block: int, H: int, k: int,
                    sm_scale: float, out, lse, ws, stream=None):
+    d = torch.cuda.current_device()
     _check("dsa_forward_q8", lib().dsa_forward_q8(
-        ctypes.byref(batch.struct), _ptr(q_idx), _ptr(k_idx), _ptr(w), H_I, _ptr(q), _ptr(kv8), _ptr(scale),
-        scale_block, H, k, sm_scale, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(batch.struct), _dev(q_idx, d), _dev(k_idx, d), _dev(w, d), H_I, _dev(q, d), _dev(kv8, d), _dev(scale, d),
+        scale_block, H, k, sm_scale, _dev(out, d), _dev(lse, d), _dev(ws, d), ws.numel(), _stream(stream)))
 
 
 def _buffers(buffers: PageBuffers | None):
@@ -386,23 +400,26 @@ def _entries(fn: str, a: torch.Tensor, b: torch.Tensor) -> int:
 def dsa_pages_resize(src: PageState, dst: PageState, seqs, new_len, buffers: PageBuffers | None, ws, stream=None):
     """Sets sequence lengths: src -> dst (the same state: in place)."""
     n = _entries("dsa_pages_resize", seqs, new_len)
+    d = torch.cuda.current_device()
     _check("dsa_pages_resize", lib().dsa_pages_resize(
-        ctypes.byref(src.struct), ctypes.byref(dst.struct), n, _ptr(seqs), _ptr(new_len), _buffers(buffers),
-        _ptr(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(src.struct), ctypes.byref(dst.struct), n, _dev(seqs, d), _dev(new_len, d), _buffers(buffers),
+        _dev(ws, d), ws.numel(), _stream(stream)))
 
 
 def dsa_pages_fork(src: PageState, dst: PageState, src_seqs, dst_seqs, ws, stream=None):
     n = _entries("dsa_pages_fork", src_seqs, dst_seqs)
+    d = torch.cuda.current_device()
     _check("dsa_pages_fork", lib().dsa_pages_fork(
-        ctypes.byref(src.struct), ctypes.byref(dst.struct), n, _ptr(src_seqs), _ptr(dst_seqs), _ptr(ws), ws.numel(),
+        ctypes.byref(src.struct), ctypes.byref(dst.struct), n, _dev(src_seqs, d), _dev(dst_seqs, d), _dev(ws, d), ws.numel(),
         _stream(stream)))
 
 
 def dsa_pages_compact(src: PageState, dst: PageState, buffers: PageBuffers | None, page_map, ws, stream=None):
     """Moves the pages in use to the front of the pool; page_map (int32 [num_pages] or
     None) receives the new place of each page that was in use."""
+    d = torch.cuda.current_device()
     _check("dsa_pages_compact", lib().dsa_pages_compact(
-        ctypes.byref(src.struct), ctypes.byref(dst.struct), _buffers(buffers), _ptr(page_map), _ptr(ws), ws.numel(),
+        ctypes.byref(src.struct), ctypes.byref(dst.struct), _buffers(buffers), _dev(page_map, d), _dev(ws, d), ws.numel(),
         _stream(stream)))
 
 

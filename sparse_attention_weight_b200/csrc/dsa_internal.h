@@ -207,7 +207,7 @@ struct PagesParams {
   int32_t* move_src;         // [num_pages]
   int32_t* move_dst;         // [num_pages]
   int32_t* old_len;          // [n]
-  int32_t* entry_ok;         // [n]
+  int32_t* last_page;        // [n]
   int32_t* start;            // [n]
   int32_t* copies;           // [n]
 };

@@ -5,8 +5,10 @@
 // only add, or take a maximum of list positions).
 //
 // Bound by latency for the bookkeeping (a few dependent passes over lists of some
-// hundred entries and the reference counts) and by memory for the copies (each
-// byte read and written once).
+// hundred entries and the reference counts), so the kernels of a call are launched
+// with programmatic dependent launch: each is resident, with its lists read, when
+// the one before it ends.  The copies are bound by memory (each byte read and
+// written once): many small chunks in flight per SM.
 #include <climits>
 
 #include "dsa_common.cuh"
@@ -17,8 +19,15 @@ namespace dsa {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kMoveThreads = 256;
-constexpr int kMoveChunk = 16384;                  // bytes of a page that a CTA copies at a time
+constexpr int kMoveThreads = 128;
+constexpr int kMoveChunk = 8192;                   // bytes of a page that a CTA copies at a time
+constexpr int kSmallPage = 512;                    // pages up to this many bytes are copied by words
+constexpr int kMaskWords = 4096;                   // pages / 32 whose masks fit in shared memory
+
+// Programmatic dependent launch: let the next kernel of the call in; wait until the
+// one before is through and its writes are visible.
+__device__ __forceinline__ void next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Exclusive prefix sum of one int per thread of the CTA; `total` gets the sum.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
@@ -50,8 +59,10 @@ __device__ __forceinline__ int pages_of(int len, int page_size) {
   return static_cast<int>((static_cast<int64_t>(len) + page_size - 1) / page_size);
 }
 
-// out = in, for the three arrays of a state.
+// out = in, for the three arrays of a state; clears the status word.
 __global__ void __launch_bounds__(256) copy_state_kernel(PagesParams p) {
+  next_kernel();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   const int64_t nt = static_cast<int64_t>(p.num_seqs) * p.pages_per_seq;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -60,138 +71,190 @@ __global__ void __launch_bounds__(256) copy_state_kernel(PagesParams p) {
   for (int64_t i = i0; i < p.num_pages; i += step) p.ref_out[i] = p.ref_in[i];
 }
 
-// One CTA works out a resize on the state `out` (which holds the input's values)
-// and lists the page copies.
-__global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p) {
+// The entry that the k-th unit of an exclusive prefix sum `start` [n] belongs to.
+__device__ __forceinline__ int owner_of(const int32_t* start, int n, int k) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= k)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// One CTA works out a resize on the state `out` (which holds the input's values once
+// the kernel before is through) and lists the page copies.  The pages that are
+// dropped and taken are spread over the threads, whichever entries they belong to.
+__global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p, bool clear) {
   __shared__ int sums[32];
   __shared__ int s_moves;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ __align__(16) int s_seq[kPlanThreads];
+  __shared__ int s_start[kPlanThreads];
+  const int tid = threadIdx.x;
   const int P = p.page_size, n = p.n;
-  if (tid == 0) s_moves = 0;
+  const int64_t top = static_cast<int64_t>(p.pages_per_seq) * P;
+  const bool few = n <= kPlanThreads;              // the lists' working copies fit in shared memory
+  int32_t* start = few ? s_start : p.start;
   uint32_t flags = 0;
-  // entry i is valid if it is the first that names its sequence
-  auto in_range = [&](int s, int len) {
-    return s >= 0 && s < p.num_seqs && len >= 0 &&
-           len <= static_cast<int64_t>(p.pages_per_seq) * P && p.len_out[s] >= 0 &&
-           p.len_out[s] <= static_cast<int64_t>(p.pages_per_seq) * P;
-  };
-  for (int i = tid; i < n; i += kPlanThreads) {
-    const int s = p.list_a[i];
-    if (s >= 0 && s < p.num_seqs) p.first[s] = INT_MAX;
-    p.old_len[i] = s >= 0 && s < p.num_seqs ? p.len_out[s] : 0;
+  next_kernel();
+  if (tid == 0) s_moves = 0;
+  // An entry is valid if it is in range and the first that names its sequence.  The
+  // first places of up to 1024 entries are found by comparing them in shared memory
+  // (one trip less than through `first`).
+  if (!few) {
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const int s = p.list_a[i];
+      if (s >= 0 && s < p.num_seqs) p.first[s] = INT_MAX;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const int s = p.list_a[i];
+      if (s >= 0 && s < p.num_seqs) atomicMin(&p.first[s], i);
+    }
+    __syncthreads();
   }
+  s_seq[tid] = few && tid < n ? p.list_a[tid] : -1;
   __syncthreads();
   for (int i = tid; i < n; i += kPlanThreads) {
-    const int s = p.list_a[i];
-    if (s >= 0 && s < p.num_seqs) atomicMin(&p.first[s], i);
-  }
-  __syncthreads();
-  auto valid = [&](int i) {
-    const int s = p.list_a[i];
-    return in_range(s, p.list_b[i]) && p.first[s] == i;
-  };
-  for (int i = tid; i < n; i += kPlanThreads) {
-    const bool ok = valid(i);
-    p.entry_ok[i] = ok;
+    const int s = few ? s_seq[i] : p.list_a[i];
+    const int want = p.list_b[i];
+    bool ok = s >= 0 && s < p.num_seqs && want >= 0 && want <= top;
+    int old = 0;
+    if (ok) {
+      old = p.len_in[s];
+      ok = old >= 0 && old <= top;
+    }
+    if (few) {
+      bool again = false;
+      for (int j = 0; j < i; j += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(&s_seq[j]);
+        again |= v.x == s || (v.y == s && j + 1 < i) || (v.z == s && j + 2 < i) || (v.w == s && j + 3 < i);
+      }
+      ok = ok && !again;
+    } else {
+      ok = ok && __ldcg(&p.first[s]) == i;
+    }
+    p.old_len[i] = ok ? old : -1;
     if (!ok) flags |= DSA_DEV_BAD_QUERY;
-  }
-  __syncthreads();
-  // shrinking entries drop their pages
-  for (int i = warp; i < n; i += kPlanThreads / 32) {
-    if (!p.entry_ok[i]) continue;
-    const int s = p.list_a[i], want = pages_of(p.list_b[i], P), have = pages_of(p.old_len[i], P);
-    int32_t* row = p.table_out + static_cast<int64_t>(s) * p.pages_per_seq;
-    for (int j = want + lane; j < have; j += 32) {
-      const int pg = row[j];
-      if (pg >= 0 && pg < p.num_pages) {
-        atomicSub(&p.ref_out[pg], 1);
-        row[j] = -1;
-      } else {
+    // growing with a partly filled last page: that page
+    int pg = -1;
+    if (ok && want > old && old % P != 0) {
+      pg = p.table_in[static_cast<int64_t>(s) * p.pages_per_seq + old / P];
+      if (pg < 0 || pg >= p.num_pages) {
         flags |= DSA_DEV_BAD_INDEX;
+        pg = -1;
+      } else {
+        p.sharers[pg] = 0;
+        p.last_sharer[pg] = -1;
       }
     }
-    if (lane == 0 && p.list_b[i] <= p.old_len[i]) p.len_out[s] = p.list_b[i];
+    p.last_page[i] = pg;
+  }
+  last_kernel();
+  if (clear && tid == 0) *p.status = 0;
+  __syncthreads();
+  // the pages behind the new lengths of shrinking entries; who shares a last page
+  int dropped = 0;
+  for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int drop = 0;
+    if (i < n && p.old_len[i] >= 0) {
+      const int old = p.old_len[i], want = p.list_b[i], pg = p.last_page[i];
+      if (want <= old) {
+        drop = pages_of(old, P) - pages_of(want, P);
+        p.len_out[p.list_a[i]] = want;
+      }
+      if (pg >= 0) {
+        atomicAdd(&p.sharers[pg], 1);
+        atomicMax(&p.last_sharer[pg], i);
+      }
+    }
+    int total;
+    const int at = block_scan(drop, sums, total);
+    if (i < n) start[i] = dropped + at;
+    dropped += total;
   }
   __syncthreads();
-  // growing entries with a partly filled last page: how many share it, and the last of them
-  auto last_page = [&](int i) {
-    if (!p.entry_ok[i] || p.list_b[i] <= p.old_len[i] || p.old_len[i] % P == 0) return -1;
-    const int pg = p.table_out[static_cast<int64_t>(p.list_a[i]) * p.pages_per_seq + p.old_len[i] / P];
-    return pg >= 0 && pg < p.num_pages ? pg : -2;
-  };
-  for (int i = tid; i < n; i += kPlanThreads) {
-    const int pg = last_page(i);
-    if (pg == -2) flags |= DSA_DEV_BAD_INDEX;
-    if (pg >= 0) {
-      p.sharers[pg] = 0;
-      p.last_sharer[pg] = -1;
+  for (int k = tid; k < dropped; k += kPlanThreads) {
+    const int i = owner_of(start, n, k);
+    int32_t* e = p.table_out + static_cast<int64_t>(p.list_a[i]) * p.pages_per_seq + pages_of(p.list_b[i], P) +
+                 (k - start[i]);
+    const int pg = *e;
+    if (pg >= 0 && pg < p.num_pages) {
+      atomicSub(&p.ref_out[pg], 1);
+      *e = -1;
+    } else {
+      flags |= DSA_DEV_BAD_INDEX;
     }
   }
   __syncthreads();
-  for (int i = tid; i < n; i += kPlanThreads) {
-    const int pg = last_page(i);
-    if (pg >= 0) {
-      atomicAdd(&p.sharers[pg], 1);
-      atomicMax(&p.last_sharer[pg], i);
-    }
-  }
-  __syncthreads();
-  // pages that each entry takes, and where its share of the free list begins
+  // pages that each entry takes, and where its share of the free list begins.  Of the
+  // growing sequences on a shared page all copy it, but for the last one if no one
+  // else holds the page.
   int need = 0;
   for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
     const int i = i0 + tid;
     int take = 0, copy = 0;
-    if (i < n && p.entry_ok[i] && p.list_b[i] > p.old_len[i]) {
-      const int pg = last_page(i);
+    if (i < n && p.list_b[i] > p.old_len[i] && p.old_len[i] >= 0) {
+      const int pg = p.last_page[i];
       if (pg >= 0) {
-        const int r = p.ref_out[pg];
-        copy = r > 1 && !(r <= p.sharers[pg] && p.last_sharer[pg] == i);
+        const int r = __ldcg(&p.ref_out[pg]);
+        copy = r > 1 && !(r <= __ldcg(&p.sharers[pg]) && __ldcg(&p.last_sharer[pg]) == i);
       }
       take = copy + pages_of(p.list_b[i], P) - pages_of(p.old_len[i], P);
     }
     int total;
     const int at = block_scan(take, sums, total);
     if (i < n) {
-      p.start[i] = need + at;
+      start[i] = need + at;
       p.copies[i] = copy;
     }
     need = need > INT_MAX - total ? INT_MAX : need + total;
   }
-  // the lowest free pages
+  // the lowest free pages, four per thread and pass
   int found = 0;
-  for (int64_t c0 = 0; c0 < p.num_pages && found < need; c0 += kPlanThreads) {
-    const int64_t pg = c0 + tid;
-    const int is_free = pg < p.num_pages && p.ref_out[pg] == 0;
+  for (int64_t c0 = 0; c0 < p.num_pages && found < need; c0 += 4 * kPlanThreads) {
+    const int64_t pg = c0 + 4 * tid;
+    int is_free[4], mine = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      is_free[u] = pg + u < p.num_pages && __ldcg(&p.ref_out[pg + u]) == 0;
+      mine += is_free[u];
+    }
     int total;
-    const int at = block_scan(is_free, sums, total);
-    if (is_free && found + at < need) p.free_list[found + at] = static_cast<int>(pg);
+    int at = found + block_scan(mine, sums, total);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (is_free[u] && at < need) p.free_list[at] = static_cast<int>(pg + u);
+      at += is_free[u];
+    }
     found += total;
   }
   __syncthreads();
   if (found < need) {
     if (tid == 0) set_status(p.status, DSA_DEV_NO_PAGES);
   } else {
-    for (int i = warp; i < n; i += kPlanThreads / 32) {
-      if (!p.entry_ok[i] || p.list_b[i] <= p.old_len[i]) continue;
-      const int s = p.list_a[i], want = pages_of(p.list_b[i], P), have = pages_of(p.old_len[i], P);
-      int32_t* row = p.table_out + static_cast<int64_t>(s) * p.pages_per_seq;
-      const int copy = p.copies[i];
-      const int* got = p.free_list + p.start[i];
-      if (copy && lane == 0) {
-        const int from = row[have - 1], to = got[0];
+    for (int i = tid; i < n; i += kPlanThreads)
+      if (p.list_b[i] > p.old_len[i] && p.old_len[i] >= 0) p.len_out[p.list_a[i]] = p.list_b[i];
+    for (int k = tid; k < need; k += kPlanThreads) {
+      const int i = owner_of(start, n, k);
+      int j = k - start[i];                        // first the copy, then the new pages
+      const int to = p.free_list[k];
+      const int have = pages_of(p.old_len[i], P);
+      int32_t* row = p.table_out + static_cast<int64_t>(p.list_a[i]) * p.pages_per_seq;
+      p.ref_out[to] = 1;
+      if (p.copies[i] && j-- == 0) {
+        const int from = p.last_page[i];
         const int m = atomicAdd(&s_moves, 1);
         p.move_src[m] = from;
         p.move_dst[m] = to;
         row[have - 1] = to;
-        p.ref_out[to] = 1;
         atomicSub(&p.ref_out[from], 1);
+      } else {
+        row[have + j] = to;
       }
-      for (int j = have + lane; j < want; j += 32) {
-        const int pg = got[copy + j - have];
-        row[j] = pg;
-        p.ref_out[pg] = 1;
-      }
-      if (lane == 0) p.len_out[s] = p.list_b[i];
     }
   }
   if (flags) set_status(p.status, flags);
@@ -202,6 +265,7 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p
 // A CTA per pair: the pair is checked against the whole list.
 __global__ void __launch_bounds__(256) fork_kernel(PagesParams p) {
   const int P = p.page_size;
+  bool waited = false;
   for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
     const int src = p.list_a[i], dst = p.list_b[i];
     bool ok = src >= 0 && src < p.num_seqs && dst >= 0 && dst < p.num_seqs;
@@ -214,6 +278,8 @@ __global__ void __launch_bounds__(256) fork_kernel(PagesParams p) {
     for (int j = threadIdx.x; j < p.n; j += blockDim.x)
       clash |= p.list_b[j] == src || (j < i && p.list_b[j] == dst);
     ok = !__syncthreads_or(clash) && ok;
+    if (!waited) last_kernel();                    // `out` is written from here on
+    waited = true;
     if (!ok) {
       if (threadIdx.x == 0) set_status(p.status, DSA_DEV_BAD_QUERY);
       continue;
@@ -236,46 +302,77 @@ __global__ void __launch_bounds__(256) fork_kernel(PagesParams p) {
 }
 
 // One CTA: the map of the pages, their new reference counts and the list of moves.
-// ref_out may be ref_in, so the counts that move are read before they are written.
+// With L pages in use, the page in use at p >= L that has r pages in use between L and
+// itself goes to the free page q < L that has r free pages below it.  A warp takes a
+// stretch of words of 32 pages; the words' masks are kept, so the counts are read once.
+// ref_out may be ref_in: the counts that move are read before they are written.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesParams p) {
   __shared__ int sums[32];
-  const int tid = threadIdx.x;
-  int live_count = 0;
-  for (int64_t c0 = 0; c0 < p.num_pages; c0 += kPlanThreads) {
-    const int64_t pg = c0 + tid;
-    live_count += __syncthreads_count(pg < p.num_pages && p.ref_in[pg] > 0);
-  }
-  // k-th page in use at or above live_count -> k-th free page below it
-  int up = 0, down = 0;
-  for (int64_t c0 = 0; c0 < p.num_pages; c0 += kPlanThreads) {
-    const int64_t pg = c0 + tid;
-    const bool in = pg < p.num_pages;
-    const bool live = in && p.ref_in[pg] > 0;
-    const int is_up = live && pg >= live_count, is_down = in && !live && pg < live_count;
-    int total;
-    int at = block_scan(is_up, sums, total);
-    if (is_up) p.move_src[up + at] = static_cast<int>(pg);
-    up += total;
-    at = block_scan(is_down, sums, total);
-    if (is_down) p.move_dst[down + at] = static_cast<int>(pg);
-    down += total;
-    if (in) {
-      p.map[pg] = live ? static_cast<int>(pg) : -1;
-      if (p.ref_out != p.ref_in) p.ref_out[pg] = p.ref_in[pg];
+  __shared__ uint32_t s_masks[kMaskWords];
+  __shared__ int s_before;                         // pages in use below page L
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int words = (p.num_pages + 31) / 32;
+  uint32_t* masks = words <= kMaskWords ? s_masks : reinterpret_cast<uint32_t*>(p.sharers);
+  const int per = (words + 31) / 32;               // words per warp
+  const int w0 = min(warp * per, words), w1 = min(w0 + per, words);
+  next_kernel();
+  if (tid == 0) *p.status = 0;
+  int count = 0;
+  for (int w = w0; w < w1; w += 4) {
+    int r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int pg = (w + u) * 32 + lane;
+      r[u] = w + u < w1 && pg < p.num_pages ? p.ref_in[pg] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (w + u >= w1) break;
+      const int pg = (w + u) * 32 + lane;
+      const uint32_t m = __ballot_sync(0xffffffffu, r[u] > 0);
+      count += __popc(m);
+      if (lane == 0) masks[w + u] = m;
+      if (pg < p.num_pages) {
+        p.map[pg] = r[u] > 0 ? pg : -1;
+        if (p.ref_out != p.ref_in) p.ref_out[pg] = r[u];
+      }
     }
   }
+  int total;
+  int before = block_scan(lane == 0 ? count : 0, sums, total);   // of lane 0: pages in use before the warp's
+  before = __shfl_sync(0xffffffffu, before, 0);
+  const int live = total;
+  if (live < p.num_pages && live / 32 >= w0 && live / 32 < w1 && lane == 0) {
+    int b = before;
+    for (int w = w0; w < live / 32; ++w) b += __popc(masks[w]);
+    s_before = b + __popc(masks[live / 32] & ((1u << (live & 31)) - 1));
+  }
+  if (live == p.num_pages && tid == 0) s_before = live;
   __syncthreads();
-  for (int i = tid; i < up; i += kPlanThreads) {
+  const int base = s_before, moves = live - base;
+  for (int w = w0; w < w1; ++w) {
+    const uint32_t m = masks[w];
+    const int pg = w * 32 + lane;
+    const bool used = m >> lane & 1;
+    const int at = before + __popc(m & ((1u << lane) - 1));
+    if (used && pg >= live) p.move_src[at - base] = pg;
+    if (!used && pg < live) p.move_dst[pg - at] = pg;
+    before += __popc(m);
+  }
+  __syncthreads();
+  for (int i = tid; i < moves; i += kPlanThreads) {
     const int from = p.move_src[i], to = p.move_dst[i];
     p.map[from] = to;
     const int r = p.ref_in[from];
     p.ref_out[to] = r;
     p.ref_out[from] = 0;
   }
-  if (tid == 0) *p.num_moves = up;
+  if (tid == 0) *p.num_moves = moves;
 }
 
 __global__ void __launch_bounds__(256) remap_kernel(PagesParams p) {
+  next_kernel();
+  last_kernel();
   const int64_t nt = static_cast<int64_t>(p.num_seqs) * p.pages_per_seq;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -295,35 +392,47 @@ __global__ void __launch_bounds__(256) remap_kernel(PagesParams p) {
     for (int64_t i = i0; i < p.num_seqs; i += step) p.len_out[i] = p.len_in[i];
 }
 
-// Copies the listed pages in all buffers, chunk by chunk.
+// Copies the listed pages in all buffers: large pages chunk by chunk, small ones a
+// run of words over several pages.
 __global__ void __launch_bounds__(kMoveThreads) move_pages_kernel(PagesParams p) {
-  const int moves = *p.num_moves;
-  const int64_t items = static_cast<int64_t>(moves) * p.chunks;
+  last_kernel();
+  const int64_t moves = __ldcg(p.num_moves);
+  const int64_t items = moves * p.chunks;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int m = static_cast<int>(it / p.chunks);
-    int c = static_cast<int>(it - static_cast<int64_t>(m) * p.chunks);
+    const int64_t m = it / p.chunks;
+    int c = static_cast<int>(it - m * p.chunks);
     int b = 0;
     while (c >= p.buf_chunks[b]) c -= p.buf_chunks[b++];
     const int64_t pb = p.buf_bytes[b];
     const int64_t o = static_cast<int64_t>(c) * kMoveChunk;
-    const int64_t n = pb - o < kMoveChunk ? pb - o : kMoveChunk;
-    const uint8_t* src = p.buf[b] + p.move_src[m] * pb + o;
-    uint8_t* dst = p.buf[b] + p.move_dst[m] * pb + o;
+    const int n = static_cast<int>(pb - o < kMoveChunk ? pb - o : kMoveChunk);
+    const uint8_t* src = p.buf[b] + __ldcg(&p.move_src[m]) * pb + o;
+    uint8_t* dst = p.buf[b] + __ldcg(&p.move_dst[m]) * pb + o;
     if (p.buf_vec[b]) {
       constexpr int kPer = kMoveChunk / 16 / kMoveThreads;
       uint4 v[kPer];
-      const int nv = static_cast<int>(n / 16);
+      const int nv = n / 16;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         if (i * kMoveThreads + static_cast<int>(threadIdx.x) < nv)
-          v[i] = reinterpret_cast<const uint4*>(src)[i * kMoveThreads + threadIdx.x];
+          v[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i * kMoveThreads + threadIdx.x);
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         if (i * kMoveThreads + static_cast<int>(threadIdx.x) < nv)
-          reinterpret_cast<uint4*>(dst)[i * kMoveThreads + threadIdx.x] = v[i];
+          __stcs(reinterpret_cast<uint4*>(dst) + i * kMoveThreads + threadIdx.x, v[i]);
     } else {
       for (int i = threadIdx.x; i < n / 4; i += kMoveThreads)
         reinterpret_cast<uint32_t*>(dst)[i] = reinterpret_cast<const uint32_t*>(src)[i];
+    }
+  }
+  for (int b = 0; b < p.num_bufs; ++b) {
+    if (p.buf_chunks[b]) continue;
+    const int64_t pw = p.buf_bytes[b] / 4;
+    uint32_t* base = reinterpret_cast<uint32_t*>(p.buf[b]);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kMoveThreads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; i < moves * pw; i += step) {
+      const int64_t m = i / pw, w = i - m * pw;
+      base[__ldcg(&p.move_dst[m]) * pw + w] = base[__ldcg(&p.move_src[m]) * pw + w];
     }
   }
 }
@@ -373,7 +482,7 @@ PagesParams pages_params(const dsa_page_state* in, const dsa_page_state* out, in
   p.move_src = take(pages);
   p.move_dst = take(pages);
   p.old_len = take(n);
-  p.entry_ok = take(n);
+  p.last_page = take(n);
   p.start = take(n);
   p.copies = take(n);
   *bytes = off;
@@ -413,31 +522,45 @@ dsa_status take_buffers(const dsa_page_buffers* bufs, PagesParams& p) {
     p.buf[j] = static_cast<uint8_t*>(bufs->base[j]);
     p.buf_bytes[j] = pb;
     p.buf_vec[j] = pb % 16 == 0 && a % 16 == 0;
-    p.buf_chunks[j] = static_cast<int>((pb + kMoveChunk - 1) / kMoveChunk);
+    p.buf_chunks[j] = pb <= kSmallPage ? 0 : static_cast<int>((pb + kMoveChunk - 1) / kMoveChunk);
     p.chunks += p.buf_chunks[j];
   }
   p.num_bufs = bufs->num;
   return DSA_OK;
 }
 
-cudaError_t launched() {
-  const cudaError_t e = cudaGetLastError();
+// Launches a kernel of a call; all but the first with programmatic dependent launch.
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), int grid, int threads, cudaStream_t st, bool first, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = first ? 0 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
 
-cudaError_t launch_copy_state(const PagesParams& p, cudaStream_t st) {
-  if (p.table_in == p.table_out) return cudaSuccess;
-  const int64_t items = static_cast<int64_t>(p.num_seqs) * p.pages_per_seq + p.num_pages;
+int grid_for(int64_t items) {
   const int64_t want = (items + 1023) / 1024, most = 8 * sm_count();
-  copy_state_kernel<<<static_cast<int>(want < most ? want : most), 256, 0, st>>>(p);
-  return launched();
+  return static_cast<int>(want < most ? want : most);
 }
 
-cudaError_t launch_moves(const PagesParams& p, cudaStream_t st) {
+cudaError_t launch_copy_state(const PagesParams& p, cudaStream_t st) {
+  return launch(copy_state_kernel, grid_for(static_cast<int64_t>(p.num_seqs) * p.pages_per_seq + p.num_pages), 256, st,
+                true, p);
+}
+
+// Copies of at most `most` pages.
+cudaError_t launch_moves(const PagesParams& p, int64_t most, cudaStream_t st) {
   if (p.num_bufs == 0) return cudaSuccess;
-  move_pages_kernel<<<8 * sm_count(), kMoveThreads, 0, st>>>(p);
-  return launched();
+  const int64_t items = most * (p.chunks > 0 ? p.chunks : 1), full = 16 * sm_count();
+  return launch(move_pages_kernel, static_cast<int>(items < full ? items : full), kMoveThreads, st, false, p);
 }
 
 dsa_status status_of(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
@@ -466,13 +589,10 @@ dsa_status dsa_pages_resize(const dsa_page_state* in, const dsa_page_state* out,
   p.list_a = seqs;
   p.list_b = new_len;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
-  cudaError_t e = launch_copy_state(p, st);
-  if (e == cudaSuccess && n > 0) {
-    resize_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
-    e = launched();
-    if (e == cudaSuccess) e = launch_moves(p, st);
-  }
+  const bool apart = p.table_in != p.table_out;
+  cudaError_t e = apart ? launch_copy_state(p, st) : cudaSuccess;
+  if (e == cudaSuccess) e = launch(resize_plan_kernel, 1, kPlanThreads, st, !apart, p, !apart);
+  if (e == cudaSuccess && n > 0) e = launch_moves(p, n, st);
   return status_of(e);
 }
 
@@ -484,12 +604,9 @@ dsa_status dsa_pages_fork(const dsa_page_state* in, const dsa_page_state* out, i
   p.list_a = src_seqs;
   p.list_b = dst_seqs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
-  cudaError_t e = launch_copy_state(p, st);
-  if (e == cudaSuccess && n > 0) {
-    fork_kernel<<<n < 4096 ? n : 4096, 256, 0, st>>>(p);
-    e = launched();
-  }
+  const bool apart = p.table_in != p.table_out;
+  cudaError_t e = apart ? launch_copy_state(p, st) : cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st);
+  if (e == cudaSuccess && n > 0) e = launch(fork_kernel, n < 4096 ? n : 4096, 256, st, !apart, p);
   return status_of(e);
 }
 
@@ -501,16 +618,10 @@ dsa_status dsa_pages_compact(const dsa_page_state* in, const dsa_page_state* out
   if (s != DSA_OK) return s;
   if (page_map) p.map = page_map;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
-  compact_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
-  cudaError_t e = launched();
-  if (e == cudaSuccess) {
-    const int64_t items = static_cast<int64_t>(p.num_seqs) * p.pages_per_seq;
-    const int64_t want = (items + 1023) / 1024, most = 8 * sm_count();
-    remap_kernel<<<static_cast<int>(want < most ? want : most), 256, 0, st>>>(p);
-    e = launched();
-  }
-  if (e == cudaSuccess) e = launch_moves(p, st);
+  cudaError_t e = launch(compact_plan_kernel, 1, kPlanThreads, st, true, p);
+  if (e == cudaSuccess)
+    e = launch(remap_kernel, grid_for(static_cast<int64_t>(p.num_seqs) * p.pages_per_seq), 256, st, false, p);
+  if (e == cudaSuccess) e = launch_moves(p, p.num_pages, st);
   return status_of(e);
 }
 
