@@ -136,6 +136,7 @@ struct ProjLayout {
   float* y;
   void* gemm_ws;
   uint16_t* kv_new;          // bf16 [T, 576] (8-bit cache only)
+  int32_t* runs;             // [T] (8-bit cache only)
   size_t bytes;
 };
 
@@ -157,6 +158,8 @@ ProjLayout proj_q8_layout(void* ws, const dsa_batch* b, int H_I, int H) {
   ProjLayout L = proj_layout(ws, b, H_I, H);
   L.kv_new = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + L.bytes);
   L.bytes += align_up(static_cast<size_t>(b->num_q) * DSA_D_QK * sizeof(uint16_t));
+  L.runs = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + L.bytes);
+  L.bytes += align_up(static_cast<size_t>(b->num_q) * sizeof(int32_t));
   return L;
 }
 
@@ -379,6 +382,11 @@ dsa_status run_project(const dsa_batch* batch, const uint16_t* hidden, const uin
 
 // ---------------------------------------------------------------- the 8-bit latent cache
 bool block_ok(int g) { return g >= 1 && g <= 64 && (g & (g - 1)) == 0; }
+int log2_of(int g) {
+  int l = 0;
+  while ((1 << l) < g) ++l;
+  return l;
+}
 bool k_q8_ok(const int32_t* idx, int k) { return idx ? k_ok(k) : k == 0; }
 bool finite(float x) { return x - x == 0.f; }
 bool rows_q8_ok(const dsa_batch* b) { return b->kv_rows < (int64_t{1} << 31); }   // the kernels keep rows in 32 bits
@@ -386,6 +394,7 @@ bool rows_q8_ok(const dsa_batch* b) { return b->kv_rows < (int64_t{1} << 31); } 
 struct Q8Layout {
   uint32_t* status;
   WsLayout fwd;              // plan, scores and idx of the forward
+  int32_t* runs;             // [T] of the append
   int splits, split_tiles;   // of the attention
   float* part_o;
   float* part_lse;
@@ -397,6 +406,10 @@ Q8Layout q8_layout(void* ws, int op, const dsa_batch* b, int H, int k) {
   uint8_t* p = static_cast<uint8_t*>(ws);
   size_t off = kWsHeader;
   L.status = reinterpret_cast<uint32_t*>(p);
+  if (op == DSA_Q8_APPEND) {
+    L.runs = reinterpret_cast<int32_t*>(p + off);
+    off += align_up(static_cast<size_t>(b->num_q) * sizeof(int32_t));
+  }
   if (op == DSA_Q8_MLA || op == DSA_Q8_FORWARD) {
     L.splits = mla_q8_plan(b->num_q, H, k > 0 ? k : b->max_kv_len, num_sms(), &L.split_tiles);
     if (L.splits > 1) {
@@ -420,13 +433,16 @@ Q8Layout q8_layout(void* ws, int op, const dsa_batch* b, int H, int k) {
   return L;
 }
 
+// The status word and the count of runs after it are 0.
 dsa_status run_quantize(const dsa_batch* b, const uint16_t* kv, uint8_t* kv8, float* scale, int block,
-                        uint32_t* status, cudaStream_t st) {
+                        uint32_t* status, int32_t* runs, cudaStream_t st) {
   QuantParams p{};
+  p.num_runs = reinterpret_cast<int32_t*>(status + 1);
+  p.runs = runs;
   p.kv = kv;
   p.kv8 = kv8;
   p.scale = scale;
-  p.block = block;
+  p.block_log2 = log2_of(block);
   p.q_seq = b->q_seq;
   p.q_pos = b->q_pos;
   p.kv_offset = b->kv_offset;
@@ -438,7 +454,7 @@ dsa_status run_quantize(const dsa_batch* b, const uint16_t* kv, uint8_t* kv8, fl
   p.kv_rows = b->kv_rows;
   p.T = b->num_q;
   p.status = status;
-  return cuda_status(launch_quantize_append(p, st));
+  return cuda_status(launch_quantize_append(p, num_sms(), st));
 }
 
 dsa_status run_mla_q8(const dsa_batch* b, const uint16_t* q, const uint8_t* kv8, const float* scale, int block,
@@ -448,7 +464,7 @@ dsa_status run_mla_q8(const dsa_batch* b, const uint16_t* q, const uint8_t* kv8,
   p.q = q;
   p.kv8 = kv8;
   p.scale = scale;
-  while ((1 << p.block_log2) < block) ++p.block_log2;
+  p.block_log2 = log2_of(block);
   p.idx = idx;
   p.k = k;
   p.H = H;
@@ -735,8 +751,8 @@ dsa_status dsa_quantize_append(const dsa_batch* batch, const uint16_t* kv, uint8
   const Q8Layout L = q8_layout(ws, DSA_Q8_APPEND, batch, 8, 0);
   if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(L.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
-  return run_quantize(batch, kv, kv8, scale, scale_block, L.status, st);
+  if (cudaMemsetAsync(L.status, 0, 2 * sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
+  return run_quantize(batch, kv, kv8, scale, scale_block, L.status, L.runs, st);
 }
 
 dsa_status dsa_project_append_q8(const dsa_batch* batch, const uint16_t* hidden, const uint16_t* w_all, int d_model,
@@ -755,10 +771,10 @@ dsa_status dsa_project_append_q8(const dsa_batch* batch, const uint16_t* hidden,
   const ProjLayout L = proj_q8_layout(ws, batch, H_I, H);
   if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(L.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
+  if (cudaMemsetAsync(L.status, 0, 2 * sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
   const dsa_status s = run_project(batch, hidden, w_all, d_model, H_I, H, rope_base, q_idx, w, q, k_idx, nullptr, L, st);
   if (s != DSA_OK) return s;
-  return run_quantize(batch, L.kv_new, kv8, scale, scale_block, L.status, st);
+  return run_quantize(batch, L.kv_new, kv8, scale, scale_block, L.status, L.runs, st);
 }
 
 dsa_status dsa_sparse_mla_q8(const dsa_batch* batch, const uint16_t* q, const uint8_t* kv8, const float* scale,

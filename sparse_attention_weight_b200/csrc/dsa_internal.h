@@ -130,7 +130,7 @@ struct QuantParams {
   const uint16_t* kv;        // [T, 576] bf16, the new rows
   uint8_t* kv8;              // [kv_rows, 576] E4M3
   float* scale;              // [ceil(kv_rows / block)]
-  int block;                 // tokens per scale
+  int block_log2;            // tokens per scale = 1 << block_log2
   const int32_t* q_seq;
   const int32_t* q_pos;
   const int64_t* kv_offset;  // contiguous layout
@@ -141,10 +141,11 @@ struct QuantParams {
   int num_seqs;
   int64_t kv_rows;
   int T;
-  int window;                // tokens that a CTA looks at
+  int32_t* num_runs;         // [1], 0 at the start
+  int32_t* runs;             // [T] tokens that begin runs
   uint32_t* status;
 };
-cudaError_t launch_quantize_append(const QuantParams& p, cudaStream_t stream);
+cudaError_t launch_quantize_append(const QuantParams& p, int sms, cudaStream_t stream);
 
 struct MlaQ8Params {
   const uint16_t* q;         // [T, H, 576] bf16

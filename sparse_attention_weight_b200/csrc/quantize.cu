@@ -8,12 +8,15 @@
 // earlier row only shifts its exponent (what falls below E4M3's smallest step is
 // rounded again).
 //
-// Bound by memory: 1152 B read and 576 B written per row, once each.  One CTA
-// (256 threads) takes a run of up to 64 new rows of one 64-position stretch (a
-// page holds whole stretches, and a stretch whole blocks), holds all of it in
-// registers between the maximum and the encoding (18 16-byte loads per thread, all
-// in flight), so the rows are read once.  A CTA finds the runs that begin in its
-// window of the token list by comparing neighbours.
+// Bound by memory: 1152 B read and 576 B written per row, once each.  The work is
+// cut into runs: the new rows of one 64-position stretch of one sequence (a page
+// holds whole stretches, and a stretch whole blocks), up to 72 KB that lie together
+// in the input.  A CTA (256 threads) brings a run into shared memory with one bulk
+// copy, takes the maximum of each block and encodes from there, so the rows are read
+// once; three CTAs per SM keep some 200 KB in flight.  Long token lists (prompts) are
+// first searched for the places where runs begin; in short ones (decode steps, where
+// nearly every token is a run) each token has its own CTA.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "dsa_common.cuh"
@@ -24,11 +27,21 @@ namespace dsa {
 namespace {
 
 constexpr int kQuantThreads = 256;
+constexpr int kWarps = kQuantThreads / 32;
 constexpr int kStretch = 64;                       // positions per run: divides every page, a multiple of every block
-constexpr int kRowChunks = DSA_D_QK / 8;           // 16-byte chunks (8 bf16) of a row
-constexpr int kWarpRows = kStretch / (kQuantThreads / 32);
-constexpr int kPer = kWarpRows * kRowChunks / 32;  // chunks per thread
+constexpr int kRowBytes = DSA_D_QK * 2;
+constexpr int kPieces = DSA_D_QK / 16;             // pieces of 16 entries of a row
 constexpr int kMinExp = -100, kMaxExp = 100;       // exponents of a scale
+constexpr int kShortList = 1024;                   // tokens up to which each has a CTA of its own
+constexpr int kCtasPerSm = 3;
+
+struct QuantSmem {
+  uint4 rows[kStretch * kRowBytes / 16];
+  uint32_t top[kStretch];                          // largest magnitude (bf16 bits) per scale block of the stretch
+  float inv[kStretch];                             // 1 / its scale
+  uint64_t full;
+};
+static_assert((sizeof(QuantSmem) + 1024) * kCtasPerSm <= 228 * 1024, "three CTAs share an SM");
 
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
@@ -39,146 +52,179 @@ __device__ __forceinline__ int need_exp(uint32_t bits) {
   return bits < 0x80u || e < kMinExp ? kMinExp : (e > kMaxExp ? kMaxExp : e);
 }
 
-__device__ __forceinline__ uint32_t max_finite(uint32_t m, uint32_t v) {
-  const uint32_t lo = v & 0x7fffu, hi = (v >> 16) & 0x7fffu;
-  if (lo < 0x7f80u && lo > m) m = lo;
-  if (hi < 0x7f80u && hi > m) m = hi;
-  return m;
+// Larger of two pairs of 16-bit magnitudes; with `finite`, infinite and NaN ones count as 0.
+__device__ __forceinline__ uint32_t max2(uint32_t m, uint32_t v, bool finite) {
+  v &= 0x7fff7fffu;
+  if (finite) v &= __vcmpltu2(v, 0x7f807f80u);
+  return __vmaxu2(m, v);
 }
 
-// Two bf16 (one word) times inv (a power of two: exact) -> two E4M3 codes.
-__device__ __forceinline__ uint32_t encode2(uint32_t v, float inv) {
-  const float2 f = make_float2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
-  return static_cast<uint16_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3));
+// Four bf16 (two words) times inv (a power of two: exact) -> four E4M3 codes.
+__device__ __forceinline__ uint32_t encode4(uint32_t a, uint32_t b, float inv) {
+  const float2 f = make_float2(inv, inv);
+  const float2 x = mul2(make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)), f);
+  const float2 y = mul2(make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)), f);
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3)) |
+         (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3)) << 16);
 }
 
 __device__ __forceinline__ uint32_t reencode4(uint32_t v, float f) {
   uint32_t r = 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const __half2_raw x =
-        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v >> (16 * h)), __NV_E4M3);
+    const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v >> (16 * h)), __NV_E4M3);
     const float2 y = __half22float2(__half2(x));
-    r |= static_cast<uint32_t>(
-             __nv_cvt_float2_to_fp8x2(make_float2(y.x * f, y.y * f), __NV_SATFINITE, __NV_E4M3))
+    r |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(y.x * f, y.y * f), __NV_SATFINITE, __NV_E4M3))
          << (16 * h);
   }
   return r;
 }
 
-__global__ void __launch_bounds__(kQuantThreads) quantize_append_kernel(QuantParams p) {
-  __shared__ uint32_t smax[kStretch];              // largest magnitude (bf16 bits) per scale block of the stretch
+// Whether token t begins a run.
+__device__ __forceinline__ bool begins_run(const QuantParams& p, int t) {
+  const int s = p.q_seq[t], x = p.q_pos[t];
+  return t == 0 || x % kStretch == 0 || p.q_seq[t - 1] != s || p.q_pos[t - 1] != x - 1;
+}
+
+// Lists the tokens that begin runs (in any order: runs do not depend on one another).
+__global__ void __launch_bounds__(256) find_runs_kernel(QuantParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int t = blockIdx.x * blockDim.x + threadIdx.x, lane = threadIdx.x & 31;
+  const bool lead = t < p.T && begins_run(p, t);
+  const uint32_t m = __ballot_sync(0xffffffffu, lead);
+  int at = 0;
+  if (lane == 0 && m) at = atomicAdd(p.num_runs, __popc(m));
+  at = __shfl_sync(0xffffffffu, at, 0);
+  if (lead) p.runs[at + __popc(m & ((1u << lane) - 1))] = t;
+}
+
+__global__ void __launch_bounds__(kQuantThreads, kCtasPerSm) quantize_append_kernel(QuantParams p) {
+  extern __shared__ __align__(128) uint8_t raw[];
+  QuantSmem& S = *reinterpret_cast<QuantSmem*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = p.block;
-  const int w0 = blockIdx.x * p.window;
-  // runs that begin in the window (every warp finds the same mask)
-  uint32_t starts;
-  {
-    const int t = w0 + lane;
-    bool lead = false;
-    if (lane < p.window && t < p.T) {
-      const int s = p.q_seq[t], x = p.q_pos[t];
-      lead = t == 0 || x % kStretch == 0 || p.q_seq[t - 1] != s || p.q_pos[t - 1] != x - 1;
-    }
-    starts = __ballot_sync(0xffffffffu, lead);
+  const int gl = p.block_log2, g = 1 << gl;
+  if (tid == 0) {
+    mbar_init(&S.full, 1);
+    fence_mbar_init();
   }
-  for (; starts; starts &= starts - 1) {
-    const int t0 = w0 + __ffs(starts) - 1;
+  if (p.runs) asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int runs = p.runs ? __ldcg(p.num_runs) : p.T;
+  __syncthreads();
+  uint32_t phase = 0;
+  for (int run = blockIdx.x; run < runs; run += gridDim.x) {
+    const int t0 = p.runs ? __ldcg(&p.runs[run]) : run;
     const int seq = p.q_seq[t0], pos = p.q_pos[t0];
+    int ps = -1, pp = 0;
+    if (t0 > 0) {
+      ps = p.q_seq[t0 - 1];
+      pp = p.q_pos[t0 - 1];
+    }
+    const bool follows = t0 > 0 && ps == seq && pp == pos - 1;
+    if (!p.runs && follows && pos % kStretch != 0) continue;      // within another token's run
     const int first = pos & (kStretch - 1);        // row of the stretch that the run begins with
-    bool ok = seq >= 0 && seq < p.num_seqs && pos >= 0 && pos < p.kv_len[seq];
-    if (ok && t0 > 0) {
-      const int ps = p.q_seq[t0 - 1];
-      ok = seq > ps || (seq == ps && p.q_pos[t0 - 1] == pos - 1);
-    }
     // rows of the run: consecutive tokens of the sequence within the stretch
-    int n = 1;
-    if (ok) {
-      uint32_t same[2];
+    uint32_t same[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int l = lane + 32 * h, t = t0 + l;
-        same[h] = __ballot_sync(0xffffffffu, t < p.T && l < kStretch - first && p.q_seq[t] == seq &&
-                                                 p.q_pos[t] == pos + l);
-      }
-      n = same[0] == 0xffffffffu ? 32 + __ffs(~same[1]) - 1 : __ffs(~same[0]) - 1;
-      if (same[0] == 0xffffffffu && same[1] == 0xffffffffu) n = 64;
+    for (int h = 0; h < 2; ++h) {
+      const int l = lane + 32 * h, t = t0 + l;
+      same[h] = __ballot_sync(0xffffffffu, t < p.T && l < kStretch - first && p.q_seq[t] == seq && p.q_pos[t] == pos + l);
     }
+    int n = ~same[0] ? __ffs(~same[0]) - 1 : 32 + (~same[1] ? __ffs(~same[1]) - 1 : 32);
+    bool ok = seq >= 0 && seq < p.num_seqs && pos >= 0 && (t0 == 0 || seq > ps || follows);
+    // the rows are on their way while the place in the cache is looked up
+    if (ok && tid == 0) {
+      mbar_arrive_expect_tx(&S.full, n * kRowBytes);
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              smem_u32(S.rows)),
+          "l"(p.kv + static_cast<int64_t>(t0) * DSA_D_QK), "r"(n * kRowBytes), "r"(smem_u32(&S.full))
+          : "memory");
+    }
+    const bool loaded = ok;
+    if (tid < kStretch) S.top[tid] = 0;
     uint32_t flag = ok ? 0u : DSA_DEV_BAD_QUERY;
-    if (ok && n > p.kv_len[seq] - pos) {
-      n = p.kv_len[seq] - pos;
-      flag = DSA_DEV_BAD_QUERY;
-    }
     int64_t row = 0;                               // cache row of the run's first token
     if (ok) {
+      const int len = p.kv_len[seq];
       if (p.page_size == 0) {
         const int64_t off = p.kv_offset[seq];
         row = off + pos;
-        if (off < 0 || off % g != 0) {
-          ok = false;
-          flag |= DSA_DEV_BAD_QUERY;
-        } else if (row + n > p.kv_rows) {
-          n = row < p.kv_rows ? static_cast<int>(p.kv_rows - row) : 0;
-          flag |= DSA_DEV_BAD_INDEX;
+        if (off < 0 || (off & (g - 1)) != 0) {
+          n = 0;
+          flag = DSA_DEV_BAD_QUERY;
         }
       } else {
         const int pg = pos / p.page_size < p.pages_per_seq
                            ? p.page_table[static_cast<int64_t>(seq) * p.pages_per_seq + pos / p.page_size]
                            : -1;
-        row = static_cast<int64_t>(pg) * p.page_size + pos % p.page_size;
-        if (pg < 0 || row >= p.kv_rows) {
-          ok = false;
-          flag |= DSA_DEV_BAD_INDEX;
-        }
+        row = pg < 0 ? p.kv_rows : static_cast<int64_t>(pg) * p.page_size + pos % p.page_size;
       }
+      if (n > len - pos) {                         // tokens beyond their sequence
+        n = max(len - pos, 0);
+        flag |= DSA_DEV_BAD_QUERY;
+      }
+      if (n > 0 && row + n > p.kv_rows) {          // rows beyond the cache (with pages: all of them)
+        n = row < p.kv_rows ? static_cast<int>(p.kv_rows - row) : 0;
+        flag |= DSA_DEV_BAD_INDEX;
+      }
+      ok = n > 0;
     }
     if (flag && tid == 0) set_status(p.status, flag);
-    if (!ok || n <= 0) continue;                   // uniform over the CTA
-
-    // the run's rows: warp w holds rows 8w .. 8w + 7 of the stretch
-    const uint4* src = reinterpret_cast<const uint4*>(p.kv + static_cast<int64_t>(t0) * DSA_D_QK);
-    uint4 v[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int c = i * 32 + lane, r = warp * kWarpRows + c / kRowChunks - first;
-      v[i] = r >= 0 && r < n ? __ldg(src + static_cast<int64_t>(r) * kRowChunks + c % kRowChunks)
-                             : make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (tid < kStretch) smax[tid] = 0;
     // the scale of the block that the run begins within, if it held rows before
-    const int b0 = first / g;
-    const int64_t blk = (row - first % g) / g;     // physical block of the run's first row
-    const bool held = first % g != 0;
+    const int b0 = first >> gl, last = (first + n - 1) >> gl;
+    const int64_t blk = (row - (first & (g - 1))) >> gl;     // physical block of the run's first row
+    const bool held = ok && (first & (g - 1)) != 0;
     const float s_old = held ? p.scale[blk] : 0.f;
     const bool s_ok = s_old >= pow2f(kMinExp) && s_old <= pow2f(kMaxExp);
     if (held && !s_ok && tid == 0) set_status(p.status, DSA_DEV_BAD_SCALE);
-    __syncthreads();
-    if (g >= kWarpRows) {                          // a warp's rows lie in one block
-      uint32_t m = 0;
+    bool done = true;
+    if (loaded) {
+      done = mbar_wait(&S.full, phase, p.status, nullptr);
+      phase ^= 1;
+    }
+    // A copy that never landed: nothing is stored, and no other run is begun (a bulk copy
+    // in flight keeps writing to this CTA's memory, so leave it one more wait).
+    if (__syncthreads_or(!done)) {
+      if (!done) mbar_wait(&S.full, phase ^ 1, p.status, nullptr);
+      __syncthreads();
+      return;
+    }
+    if (!ok) continue;
+    // largest entries per block: warp w takes the run's rows w, w + 8, ...
+    for (int i = warp; i < n; i += kWarps) {
+      const uint4* src = S.rows + i * (kRowBytes / 16);
+      auto largest = [&](bool finite) {
+        uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        m = max_finite(max_finite(max_finite(max_finite(m, v[i].x), v[i].y), v[i].z), v[i].w);
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0 && m) atomicMax(&smax[warp * kWarpRows / g], m);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const uint32_t m = max_finite(max_finite(max_finite(max_finite(0, v[i].x), v[i].y), v[i].z), v[i].w);
-        if (m) atomicMax(&smax[(warp * kWarpRows + (i * 32 + lane) / kRowChunks) / g], m);
-      }
+        for (int u = 0; u < 3; ++u) {
+          const int c = u * 32 + lane;
+          if (c < kRowBytes / 16) {
+            const uint4 v = src[c];
+            m = max2(max2(max2(max2(m, v.x, finite), v.y, finite), v.z, finite), v.w, finite);
+          }
+        }
+        return __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+      };
+      uint32_t m = largest(false);
+      if (m >= 0x7f80u) m = largest(true);         // an infinity or NaN is among them
+      if (lane == 0 && m) atomicMax(&S.top[(first + i) >> gl], m);
     }
     __syncthreads();
-    // scale of a block of the stretch
-    auto block_scale = [&](int b) {
-      const float need = pow2f(need_exp(smax[b]));
-      return b == b0 && s_ok ? fmaxf(need, s_old) : need;
-    };
+    float s0 = 0.f;                                // scale of the first block
+    {
+      const float need = pow2f(need_exp(S.top[b0]));
+      s0 = s_ok ? fmaxf(need, s_old) : need;
+    }
+    if (tid >= b0 && tid <= last) {
+      const float s = tid == b0 ? s0 : pow2f(need_exp(S.top[tid]));
+      p.scale[blk + tid - b0] = s;
+      S.inv[tid] = 1.f / s;
+    }
     // earlier rows of the first block, when its scale grows
-    const float s0 = block_scale(b0);
-    if (held && s_ok && s0 > s_old) {
+    if (s_ok && s0 > s_old) {
       const float f = s_old / s0;
       uint4* dst = reinterpret_cast<uint4*>(p.kv8 + blk * g * DSA_D_QK);
-      for (int i = tid; i < (first % g) * (DSA_D_QK / 16); i += kQuantThreads) {
+      for (int i = tid; i < (first & (g - 1)) * (DSA_D_QK / 16); i += kQuantThreads) {
         uint4 c = dst[i];
         c.x = reencode4(c.x, f);
         c.y = reencode4(c.y, f);
@@ -187,33 +233,47 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_append_kernel(QuantPar
         dst[i] = c;
       }
     }
-    // codes of the new rows
-    uint8_t* out = p.kv8 + row * DSA_D_QK;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int c = i * 32 + lane, rs = warp * kWarpRows + c / kRowChunks, r = rs - first;
-      if (r < 0 || r >= n) continue;
-      const float inv = 1.f / block_scale(rs / g);
-      *reinterpret_cast<uint2*>(out + static_cast<int64_t>(r) * DSA_D_QK + (c % kRowChunks) * 8) =
-          make_uint2(encode2(v[i].x, inv) | (encode2(v[i].y, inv) << 16),
-                     encode2(v[i].z, inv) | (encode2(v[i].w, inv) << 16));
+    __syncthreads();
+    // codes of the new rows, 16 per thread and step
+    uint4* out = reinterpret_cast<uint4*>(p.kv8 + row * DSA_D_QK);
+    for (int c = tid; c < n * kPieces; c += kQuantThreads) {
+      const float inv = S.inv[(first + c / kPieces) >> gl];
+      const uint4 a = S.rows[2 * c], b = S.rows[2 * c + 1];
+      out[c] = make_uint4(encode4(a.x, a.y, inv), encode4(a.z, a.w, inv), encode4(b.x, b.y, inv), encode4(b.z, b.w, inv));
     }
-    const int last = (first + n - 1) / g;
-    if (tid >= b0 && tid <= last) p.scale[blk + tid - b0] = block_scale(tid);
-    __syncthreads();                               // smax is reset by the next run
+    __syncthreads();                               // the rows and tables are free for the next run
   }
 }
 
 }  // namespace
 
-cudaError_t launch_quantize_append(const QuantParams& params, cudaStream_t stream) {
+cudaError_t launch_quantize_append(const QuantParams& params, int sms, cudaStream_t stream) {
   if (params.T == 0) return cudaSuccess;
   QuantParams p = params;
-  // A long list is mostly prompts (a run per 64 tokens), so a CTA looks at 16
-  // tokens; in a short one every token may be a run of its own.
-  p.window = p.T > 4096 ? 16 : 1;
-  quantize_append_kernel<<<(p.T + p.window - 1) / p.window, kQuantThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const size_t smem = sizeof(QuantSmem);
+  cudaError_t e =
+      cudaFuncSetAttribute(quantize_append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.blockDim = dim3(kQuantThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at = {};
+  if (p.T <= kShortList) {
+    p.runs = nullptr;
+    cfg.gridDim = dim3(p.T);
+  } else {
+    find_runs_kernel<<<(p.T + 255) / 256, 256, 0, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    count_launches(1);
+    const int most = kCtasPerSm * sms;
+    cfg.gridDim = dim3(p.T < most ? p.T : most);
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+  }
+  e = cudaLaunchKernelEx(&cfg, quantize_append_kernel, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

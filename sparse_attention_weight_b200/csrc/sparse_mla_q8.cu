@@ -35,6 +35,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 
@@ -169,24 +171,6 @@ __device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& phase, int lane, u
   ++phase;
   __syncwarp();
   return ok;
-}
-
-// Packed fp32 pairs, each lane rounded like the scalar operation.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
 }
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -925,6 +909,25 @@ __global__ void __launch_bounds__(128) combine_kernel(MlaQ8Params p) {
 
 }  // namespace
 
+// Once per device: the kernel's shared memory, and that it was built at the register
+// count that its split adds up to (with fewer, an increase would never be granted).
+static cudaError_t prepare_device(size_t smem) {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(mla_q8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, mla_q8_kernel);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  ready.fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
+}
+
 // Splits of the row lists: with few queries a list is cut so that its parts fill
 // the SMs.  The choice minimises (waves of items) x (tiles of an item + 3): an item
 // costs about three tiles' time beside its tiles (the queries' split, the first
@@ -952,15 +955,8 @@ cudaError_t launch_sparse_mla_q8(const MlaQ8Params& params, int sms, cudaStream_
   MlaQ8Params p = params;
   if (p.T == 0) return cudaSuccess;
   const size_t smem = sizeof(Q8Smem);
-  cudaError_t e = cudaFuncSetAttribute(mla_q8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = prepare_device(smem);
   if (e != cudaSuccess) return e;
-  // The register split adds up only at kLaunchRegs per thread: with fewer, an
-  // increase would never be granted.
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, mla_q8_kernel);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
   p.groups = (p.H + kHT - 1) / kHT;
   const int64_t items = static_cast<int64_t>(p.T) * p.splits * p.groups;
   if (items > 0x7fffffff - sms) return cudaErrorInvalidConfiguration;
