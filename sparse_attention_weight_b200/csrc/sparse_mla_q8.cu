@@ -306,7 +306,6 @@ __device__ __forceinline__ bool split_queries(const MlaQ8Params& p, Q8Smem& S, i
   const bool ok = ord == 0 || wait(&S.l_full, (ord - 1) & 1, p.status, &S.abort);
   if (lane < kPer) S.qs[w0 + lane * kSoftWarps] = qs;
   __syncwarp();
-  if (lane == 0) mbar_arrive(&S.q_full);
   return ok;
 }
 
@@ -350,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, S.tmem, 0);
+  if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine may queue up
   const int step = gridDim.x;
 
   if (warp < kSoftWarps) {
@@ -364,18 +364,23 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     bool bad = false;                               // a wait ran out
     int tiles_next = 0;                             // tiles of the next item
     // the tiles of the kk-th item, and its queries' operand if it has any
+    // (of the first item before its tiles are known: there is nothing to wait for)
     auto next_queries = [&](int kk, int it) {
+      Item I;
+      item_place(p, it, I);
+      if (kk == 0) split_queries(p, S, I.t, I.hg, 0, warp, lane);
       bad |= !wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
       tiles_next = S.plan[kk & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
       if (tiles_next == 0) return;
-      // the products of the last item have read its queries
-      bad |= nq > 0 && !wait(&S.q_free, (nq - 1) & 1, p.status, ab);
-      __syncwarp();
-      Item I;
-      item_place(p, it, I);
-      bad |= !split_queries(p, S, I.t, I.hg, nq, warp, lane);
+      if (kk > 0) {
+        // the products of the last item have read its queries
+        bad |= nq > 0 && !wait(&S.q_free, (nq - 1) & 1, p.status, ab);
+        __syncwarp();
+        bad |= !split_queries(p, S, I.t, I.hg, nq, warp, lane);
+      }
+      if (lane == 0) mbar_arrive(&S.q_full);
     };
     if (blockIdx.x < p.items) next_queries(0, blockIdx.x);
     for (int kk = 0, it = blockIdx.x; it < p.items; ++kk, it += step) {
@@ -868,6 +873,7 @@ __global__ void __launch_bounds__(128) combine_kernel(MlaQ8Params p) {
   __shared__ float s_lse;
   const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   const int64_t at = static_cast<int64_t>(t) * p.splits * p.H + h;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are complete
   if (tid < 32) {
     float v[2], mx = -INFINITY;
 #pragma unroll
@@ -966,8 +972,16 @@ cudaError_t launch_sparse_mla_q8(const MlaQ8Params& params, int sms, cudaStream_
   if (e != cudaSuccess) return e;
   count_launches(1);
   if (p.splits == 1) return e;
-  combine_kernel<<<dim3(p.T, p.H), 128, 0, stream>>>(p);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.T, p.H);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, combine_kernel, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
