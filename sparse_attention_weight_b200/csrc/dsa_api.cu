@@ -411,7 +411,11 @@ Q8Layout q8_layout(void* ws, int op, const dsa_batch* b, int H, int k) {
     off += align_up(static_cast<size_t>(b->num_q) * sizeof(int32_t));
   }
   if (op == DSA_Q8_MLA || op == DSA_Q8_FORWARD) {
-    L.splits = mla_q8_plan(b->num_q, H, k > 0 ? k : b->max_kv_len, num_sms(), &L.split_tiles);
+    // lists of k entries, or of whole contexts, whose mean the cache's rows bound
+    const int64_t mean = b->kv_rows / b->num_seqs;
+    L.splits = k > 0 ? mla_q8_plan(b->num_q, H, k, k, num_sms(), &L.split_tiles)
+                     : mla_q8_plan(b->num_q, H, b->max_kv_len, mean < b->max_kv_len ? mean : b->max_kv_len, num_sms(),
+                                   &L.split_tiles);
     if (L.splits > 1) {
       const size_t rows = static_cast<size_t>(b->num_q) * L.splits * H;
       L.part_o = reinterpret_cast<float*>(p + off);
@@ -457,6 +461,7 @@ dsa_status run_quantize(const dsa_batch* b, const uint16_t* kv, uint8_t* kv8, fl
   return cuda_status(launch_quantize_append(p, num_sms(), st));
 }
 
+// The status word and the item counter after it are 0.
 dsa_status run_mla_q8(const dsa_batch* b, const uint16_t* q, const uint8_t* kv8, const float* scale, int block,
                       const int32_t* idx, int k, int H, float sm_scale, uint16_t* out, float* lse, const Q8Layout& L,
                       cudaStream_t st) {
@@ -484,6 +489,7 @@ dsa_status run_mla_q8(const dsa_batch* b, const uint16_t* q, const uint8_t* kv8,
   p.status = L.status;
   p.splits = L.splits;
   p.split_tiles = L.split_tiles;
+  p.counter = reinterpret_cast<int32_t*>(L.status + 1);
   p.part_o = L.part_o;
   p.part_lse = L.part_lse;
   return cuda_status(launch_sparse_mla_q8(p, num_sms(), st));
@@ -788,7 +794,7 @@ dsa_status dsa_sparse_mla_q8(const dsa_batch* batch, const uint16_t* q, const ui
   const Q8Layout L = q8_layout(ws, DSA_Q8_MLA, batch, H, k);
   if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(L.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
+  if (cudaMemsetAsync(L.status, 0, 2 * sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
   return run_mla_q8(batch, q, kv8, scale, scale_block, idx, k, H, sm_scale, out, lse, L, st);
 }
 
@@ -806,7 +812,7 @@ dsa_status dsa_forward_q8(const dsa_batch* batch, const uint8_t* q_idx, const ui
   const Q8Layout L = q8_layout(ws, DSA_Q8_FORWARD, batch, H, k);
   if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(L.status, 0, sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
+  if (cudaMemsetAsync(L.status, 0, 2 * sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
   const int64_t ld = default_ld(batch);
   dsa_status s = run_indexer(batch, q_idx, k_idx, w, H_I, L.fwd.scores, ld, L.fwd, st);
   if (s != DSA_OK) return s;

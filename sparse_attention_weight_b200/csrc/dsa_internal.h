@@ -173,11 +173,12 @@ struct MlaQ8Params {
   int split_tiles;           // 128-row tiles of a part
   int groups;                // head groups
   int items;                 // T * splits * groups
+  int32_t* counter;          // items handed out, 0 at the start
   float* part_o;             // [T, splits, H, 512] fp32 (splits > 1)
   float* part_lse;           // [T, splits, H]       fp32 (splits > 1)
 };
 // Parts that each query's row list is cut into, and the 128-row tiles of a part.
-int mla_q8_plan(int T, int H, int max_entries, int sms, int* split_tiles);
+int mla_q8_plan(int T, int H, int64_t most, int64_t mean, int sms, int* split_tiles);
 cudaError_t launch_sparse_mla_q8(const MlaQ8Params& p, int sms, cudaStream_t stream);
 
 struct PagesParams {

@@ -19,7 +19,8 @@
 // passes 2^8.5.  A weight has 8 significant bits down to 2^-7 of that largest one
 // and an absolute error of at most 2^-15 of it below.
 //
-// One CTA per SM works through items (query, 64 heads, split of the row list).
+// One CTA per SM works through items (query, 64 heads, split of the row list), the
+// first by its index and the others off a counter (lists are ragged).
 // TMEM (512 columns): two S^T buffers of 128 columns, O^T as 4 x 64 columns.
 // Shared memory (227 KB): Q 72 KB, two row tiles of 72 KB, W_lo 8 KB; W_hi lies over
 // the row tile's RoPE part, which only the first product reads.  The second product
@@ -78,7 +79,8 @@ struct Q8Smem {
   uint64_t rows_full[2], rows_empty[2][4], s_full[2], s_free[2], w_full[4], q_full, q_free, o_full, o_free, l_full, l_free,
       plan_full[2], plan_free[2], vote[kGroups], sync[kGroups], gather_sync, done;
   int over[kGroups][2];                            // a weight of the group passed the limit (by tile parity)
-  int plan[2];                                     // tiles of the item
+  int plan[2], item[2];                            // tiles of an item and its number, -1 after the last
+  int drawn[2];                                    // item numbers on their way to the gather warps
   int last[kGatherWarps];
   uint32_t tmem;
   int abort;
@@ -217,11 +219,13 @@ struct Item {
   bool ok;
 };
 
+// Items go head group by head group (neighbours share their rows in L2), query by query,
+// and part by part of the lists, so that the parts that short lists lack come last.
 __device__ __forceinline__ void item_place(const MlaQ8Params& p, int it, Item& I) {
   I.hg = it % p.groups;
   const int r = it / p.groups;
-  I.sp = r % p.splits;
-  I.t = r / p.splits;
+  I.t = r % p.T;
+  I.sp = r / p.T;
 }
 
 __device__ __forceinline__ void item_list(const MlaQ8Params& p, Item& I) {
@@ -350,7 +354,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, S.tmem, 0);
   if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine may queue up
-  const int step = gridDim.x;
 
   if (warp < kSoftWarps) {
     // ================================================================ softmax
@@ -362,29 +365,33 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     const float c0 = p.sm_scale * 1.4426950408889634f;
     uint32_t g = 0, nq = 0, met = 0, votes = 0;     // tiles, non-empty items, meetings, votes so far
     bool bad = false;                               // a wait ran out
-    int tiles_next = 0;                             // tiles of the next item
-    // the tiles of the kk-th item, and its queries' operand if it has any
-    // (of the first item before its tiles are known: there is nothing to wait for)
-    auto next_queries = [&](int kk, int it) {
+    int tiles = 0;                                  // of the item
+    // Into the kk-th item, with its queries' operand if it has rows (of the first item
+    // before its tiles are known: there is nothing to wait for).  False after the last.
+    auto enter = [&](int kk) {
       Item I;
-      item_place(p, it, I);
-      if (kk == 0) split_queries(p, S, I.t, I.hg, 0, warp, lane);
+      if (kk == 0) {
+        item_place(p, blockIdx.x, I);
+        split_queries(p, S, I.t, I.hg, 0, warp, lane);
+      }
       bad |= !wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
-      tiles_next = S.plan[kk & 1];
+      tiles = S.plan[kk & 1];
+      const int it = S.item[kk & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
-      if (tiles_next == 0) return;
+      if ((bad = __any_sync(0xffffffffu, bad)) || it < 0) return false;
+      if (tiles == 0) return true;
       if (kk > 0) {
         // the products of the last item have read its queries
         bad |= nq > 0 && !wait(&S.q_free, (nq - 1) & 1, p.status, ab);
         __syncwarp();
+        item_place(p, it, I);
         bad |= !split_queries(p, S, I.t, I.hg, nq, warp, lane);
       }
       if (lane == 0) mbar_arrive(&S.q_full);
+      return true;
     };
-    if (blockIdx.x < p.items) next_queries(0, blockIdx.x);
-    for (int kk = 0, it = blockIdx.x; it < p.items; ++kk, it += step) {
-      const int tiles = tiles_next;
+    for (int kk = 0; enter(kk); ++kk) {
       float l[kGH];
 #pragma unroll
       for (int i = 0; i < kGH; ++i) l[i] = 0.f;
@@ -539,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.l_full);
       }
-      if (it + step < p.items) next_queries(kk + 1, it + step);
     }
   } else if (warp < kSoftWarps + kGatherWarps) {
     // ================================================================ rows
@@ -547,7 +553,22 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     const int gw = warp - kSoftWarps, gt = tid - 32 * kSoftWarps;
     uint32_t g = 0, met = 0;
     bool bad = false;                               // a wait ran out
-    for (int kk = 0, it = blockIdx.x; it < p.items && !bad; ++kk, it += step) {
+    int next = 0;                                   // of the first thread: the next item
+    for (int kk = 0, it = blockIdx.x; !bad; ++kk) {
+      if (kk > 0) {
+        if (gt == 0) S.drawn[kk & 1] = next;
+        bad |= !meet(&S.gather_sync, met, lane, p.status, ab);
+        it = S.drawn[kk & 1];
+      }
+      if (it >= p.items) {
+        if (gt == 0) {
+          bad |= kk > 1 && !wait(&S.plan_free[kk & 1], ((kk - 2) >> 1) & 1, p.status, ab);
+          S.item[kk & 1] = -1;
+          S.plan[kk & 1] = 0;
+          mbar_arrive(&S.plan_full[kk & 1]);
+        }
+        break;
+      }
       Item I;
       item_place(p, it, I);
       item_list(p, I);
@@ -605,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       if (gt == 0) {
         bad |= kk > 1 && !wait(&S.plan_free[kk & 1], ((kk - 2) >> 1) & 1, p.status, ab);
         S.plan[kk & 1] = tiles;
+        S.item[kk & 1] = it;
         mbar_arrive(&S.plan_full[kk & 1]);
       }
       float sc = scale_of(row);
@@ -650,9 +672,24 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         }
         ++g;
       };
+      if (gt == 0 && tiles == 0) next = gridDim.x + atomicAdd(p.counter, 1);
       for (int j = 0; j < tiles; ++j) {
+        // The next item is drawn late (a CTA at the start of a long list would take it from an
+        // idle one), but early enough that its number is there when the last rows are out.
+        if (gt == 0 && (j == tiles - 2 || tiles == 1)) next = gridDim.x + atomicAdd(p.counter, 1);
         gather(j);
         if ((bad = __any_sync(0xffffffffu, bad))) break;
+        if (j == tiles - 1 && gw == 0) {            // its queries on their way to L2
+          const int n = __shfl_sync(0xffffffffu, next, 0);
+          if (n < p.items) {
+            Item N;
+            item_place(p, n, N);
+            const int lines = min(kHT, p.H - N.hg * kHT) * (DSA_D_QK * 2 / 128);
+            const char* src =
+                reinterpret_cast<const char*>(p.q + (static_cast<int64_t>(N.t) * p.H + N.hg * kHT) * DSA_D_QK);
+            for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i * 128));
+          }
+        }
       }
       bad = __any_sync(0xffffffffu, bad);
     }
@@ -665,20 +702,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     const uint32_t o_at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kOCol;
     uint32_t nq = 0;
     bool bad = false;
-    for (int kk = 0, it = blockIdx.x; it < p.items; ++kk, it += step) {
-      if (it + step < p.items) {                    // the next item's queries on their way to L2
-        Item N;
-        item_place(p, it + step, N);
-        const int lines = min(kHT, p.H - N.hg * kHT) * (DSA_D_QK * 2 / 128);
-        const char* src =
-            reinterpret_cast<const char*>(p.q + (static_cast<int64_t>(N.t) * p.H + N.hg * kHT) * DSA_D_QK);
-        for (int i = r; i < lines; i += 32 * kOutWarps)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i * 128));
-      }
+    for (int kk = 0;; ++kk) {
       bad |= !wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
       const bool any = S.plan[kk & 1] > 0;
+      const int it = S.item[kk & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
+      if ((bad = __any_sync(0xffffffffu, bad)) || it < 0) break;
       Item I;
       item_place(p, it, I);
       const int h0 = I.hg * kHT;
@@ -786,12 +816,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     if (warp == kSoftWarps + kGatherWarps + kOutWarps) {
       // ================================================================ S^T = codes . Q^T
       constexpr uint32_t id = instr_desc(0, 0, false, false, 128, 2 * kHT);
-      for (int kk = 0, it = blockIdx.x; it < p.items && ok; ++kk, it += step) {
+      for (int kk = 0; ok; ++kk) {
         ok = wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
-        const int tiles = __shfl_sync(0xffffffffu, S.plan[kk & 1], 0);
+        const int tiles = __shfl_sync(0xffffffffu, S.plan[kk & 1], 0), it = S.item[kk & 1];
+        __syncwarp();
         if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
         if (tiles > 0) ok = ok && wait(&S.q_full, n & 1, p.status, ab);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (!(ok = __all_sync(0xffffffffu, ok && it >= 0))) break;
         if (tiles == 0) continue;
         ++n;
         for (int j = 0; j < tiles; ++j, ++g) {
@@ -822,12 +853,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
     } else if (warp == kSoftWarps + kGatherWarps + kOutWarps + 1) {
       // ================================================================ O^T += codes^T . W
       constexpr uint32_t id = instr_desc(0, 0, true, true, 128, kHT);
-      for (int kk = 0, it = blockIdx.x; it < p.items && ok; ++kk, it += step) {
+      for (int kk = 0; ok; ++kk) {
         ok = wait(&S.plan_full[kk & 1], (kk >> 1) & 1, p.status, ab);
-        const int tiles = __shfl_sync(0xffffffffu, S.plan[kk & 1], 0);
+        const int tiles = __shfl_sync(0xffffffffu, S.plan[kk & 1], 0), it = S.item[kk & 1];
+        __syncwarp();
         if (lane == 0) mbar_arrive(&S.plan_free[kk & 1]);
         if (tiles > 0 && n > 0) ok = ok && wait(&S.o_free, (n - 1) & 1, p.status, ab);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (!(ok = __all_sync(0xffffffffu, ok && it >= 0))) break;
         if (tiles == 0) continue;
         ++n;
         for (int j = 0; j < tiles && ok; ++j, ++g) {
@@ -934,27 +966,31 @@ static cudaError_t prepare_device(size_t smem) {
   return cudaSuccess;
 }
 
-// Splits of the row lists: with few queries a list is cut so that its parts fill
-// the SMs.  The choice minimises (waves of items) x (tiles of an item + 3): an item
-// costs about three tiles' time beside its tiles (the queries' split, the first
-// row latencies, the output).
-int mla_q8_plan(int T, int H, int max_entries, int sms, int* split_tiles) {
+// Splits of the row lists: with few queries a list is cut so that its parts fill the
+// SMs.  `most` and `mean` are the longest list and the mean one.  An item costs about
+// three tiles' time beside its tiles (the first row latencies, the first reference,
+// the output).  Where the items go round once, the time is that of one item;
+// otherwise that of an even share, and one item at the end.  (Decode of 24 contexts
+// of 1 .. 8191 rows, dense: parts of 21 tiles 68 us, of 11 tiles 83 us, of 14 as chosen
+// here: see the measurements.)
+int mla_q8_plan(int T, int H, int64_t most, int64_t mean, int sms, int* split_tiles) {
   const int64_t base = static_cast<int64_t>(T) * ((H + kHT - 1) / kHT);
-  const int tiles = max_entries > 0 ? (max_entries + kRows - 1) / kRows : 1;
-  int best = 1, best_tiles = tiles;
-  int64_t best_cost = -1;
-  for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
-    const int per = (tiles + s - 1) / s;
-    if ((tiles + per - 1) / per != s) continue;
-    const int64_t cost = (base * s + sms - 1) / sms * (per + 3);
+  const int64_t tiles = most > 0 ? (most + kRows - 1) / kRows : 1;
+  const int64_t mean_tiles = mean > 0 ? (mean + kRows - 1) / kRows : 1;
+  int64_t best = tiles, best_cost = -1;
+  for (int64_t s = 1; s <= kMaxSplits && s <= tiles; ++s) {
+    const int64_t per = (tiles + s - 1) / s;
+    // parts of lists of one length, or of ragged ones (half a part more per list)
+    const int64_t items =
+        mean_tiles == tiles ? base * ((tiles + per - 1) / per) : (base * (2 * mean_tiles + per) + 2 * per - 1) / (2 * per);
+    const int64_t cost = items <= sms ? per + 3 : (base * mean_tiles + 3 * items + sms - 1) / sms + (s > 1 ? per : 3);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
-      best = s;
-      best_tiles = per;
+      best = per;
     }
   }
-  *split_tiles = best_tiles;
-  return best;
+  *split_tiles = static_cast<int>(best);
+  return static_cast<int>((tiles + best - 1) / best);
 }
 
 cudaError_t launch_sparse_mla_q8(const MlaQ8Params& params, int sms, cudaStream_t stream) {
