@@ -140,16 +140,22 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x1) : "f"(d), "f"(c));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(x0), "r"(x0 & 0xff80ff80u));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(x1), "r"(x1 & 0xff80ff80u));
-  uint32_t h0 = twice_plus(x0, 0), h1 = twice_plus(x1, 0);
-  uint32_t l0 = twice_plus(r0, 0x00800080u), l1 = twice_plus(r1, 0x00800080u);
-  if (kSigned) {                                    // the doubling moved the signs out
-    h0 |= x0 & 0x80008000u;
-    h1 |= x1 & 0x80008000u;
-    l0 |= r0 & 0x80008000u;
-    l1 |= r1 & 0x80008000u;
+  hi = __byte_perm(twice_plus(x0, 0), twice_plus(x1, 0), 0x7531);
+  lo = __byte_perm(twice_plus(r0, 0x00800080u), twice_plus(r1, 0x00800080u), 0x7531);
+  if (kSigned) {                                    // the doubling moved the signs out; lo's is hi's
+    const uint32_t sign = __byte_perm(x0, x1, 0x7531);
+    hi |= sign & 0x80808080u;
+    lo |= sign & 0x80808080u;
   }
-  hi = __byte_perm(h0, h1, 0x7531);
-  lo = __byte_perm(l0, l1, 0x7531);
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
+
+// Two bf16 -> fp32 (the lower one shifted up on the multiply pipe).
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  uint32_t lo;
+  asm("mad.lo.u32 %0, %1, 65536, 0;" : "=r"(lo) : "r"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(v & 0xffff0000u));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -262,10 +268,11 @@ __device__ __forceinline__ bool split_queries(const MlaQ8Params& p, Q8Smem& S, i
       v[i] = hl < heads && (i < 4 || lane < 16) ? __ldg(src + i * 32) : make_uint2(0u, 0u);
   };
   auto split = [&](int hl, const uint2(&v)[5]) -> float {
-    uint32_t am = 0;                                // two 16-bit maxima
+    __nv_bfloat162 top = __habs2(as_bf16x2(v[0].x));
 #pragma unroll
-    for (int i = 0; i < 5; ++i) am = __vmaxu2(am, __vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu));
-    am = __reduce_max_sync(0xffffffffu, max(am & 0xffffu, am >> 16));
+    for (int i = 0; i < 5; ++i) top = __hmax2_nan(top, __hmax2_nan(__habs2(as_bf16x2(v[i].x)), __habs2(as_bf16x2(v[i].y))));
+    const uint32_t two = *reinterpret_cast<const uint32_t*>(&top) & 0x7fff7fffu;
+    const uint32_t am = __reduce_max_sync(0xffffffffu, max(two & 0xffffu, two >> 16));
     // times 2^e: the largest entry in [2^-1, 1)
     int e = 126 - static_cast<int>(am >> 7);
     if (e > 118) e = 118;
@@ -275,10 +282,7 @@ __device__ __forceinline__ bool split_queries(const MlaQ8Params& p, Q8Smem& S, i
     uint8_t* rope = &S.q.rope[hl * 64 + (((lane >> 2) & 3) ^ ((hl >> 1) & 3)) * 16 + (lane & 3) * 4];
 #pragma unroll
     for (int i = 0; i < 5; ++i) {
-      const float2 a = mul2(make_float2(__uint_as_float(v[i].x << 16), __uint_as_float(v[i].x & 0xffff0000u)),
-                            make_float2(up, up));
-      const float2 b = mul2(make_float2(__uint_as_float(v[i].y << 16), __uint_as_float(v[i].y & 0xffff0000u)),
-                            make_float2(up, up));
+      const float2 a = mul2(unpack2(v[i].x), make_float2(up, up)), b = mul2(unpack2(v[i].y), make_float2(up, up));
       uint32_t hi, lo;
       split4<true>(a.x, a.y, b.x, b.y, hi, lo);
       if (bad) hi = 0x7f7f7f7fu;
@@ -970,9 +974,9 @@ static cudaError_t prepare_device(size_t smem) {
 // SMs.  `most` and `mean` are the longest list and the mean one.  An item costs about
 // three tiles' time beside its tiles (the first row latencies, the first reference,
 // the output).  Where the items go round once, the time is that of one item;
-// otherwise that of an even share, and one item at the end.  (Decode of 24 contexts
-// of 1 .. 8191 rows, dense: parts of 21 tiles 68 us, of 11 tiles 83 us, of 14 as chosen
-// here: see the measurements.)
+// otherwise that of an even share, and one item at the end: 24 contexts of 1 .. 8191
+// rows, dense, take 60 us in the parts of 12 tiles chosen here and 68 us in parts of 20
+// that go round once.
 int mla_q8_plan(int T, int H, int64_t most, int64_t mean, int sms, int* split_tiles) {
   const int64_t base = static_cast<int64_t>(T) * ((H + kHT - 1) / kHT);
   const int64_t tiles = most > 0 ? (most + kRows - 1) / kRows : 1;
