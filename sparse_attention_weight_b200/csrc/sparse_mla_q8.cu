@@ -407,14 +407,15 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
       for (int j = 0; j < tiles; ++j, ++g) {
         const int b = g & 1;
         const uint32_t ph = (g >> 1) & 1;
-        bad |= !wait(&S.rows_full[b], ph, p.status, ab) || !wait(&S.s_full[b], ph, p.status, ab);
-        if ((bad = __any_sync(0xffffffffu, bad))) break;
-        tc_fence_after();
+        bad |= !wait(&S.rows_full[b], ph, p.status, ab);
         const float s = S.s_row[b][r];
         const bool usable = s > 0.f;
         const float c = c0 * s;
         const float sg = usable ? lg2_approx(s) : -INFINITY;
         const float inv = usable ? rcp_approx(s) : 0.f;
+        bad |= !wait(&S.s_full[b], ph, p.status, ab);
+        if ((bad = __any_sync(0xffffffffu, bad))) break;
+        tc_fence_after();
         uint32_t wh[4], wl[4];
         float x[kGH];                               // log2 of the weight, then the weight
         auto logits = [&]() {
