@@ -387,7 +387,8 @@ int log2_of(int g) {
   while ((1 << l) < g) ++l;
   return l;
 }
-bool k_q8_ok(const int32_t* idx, int k) { return idx ? k_ok(k) : k == 0; }
+// The sparse form has a list, the dense one k = 0; an empty batch may have no pointers.
+bool k_q8_ok(const dsa_batch* b, const int32_t* idx, int k) { return k == 0 ? !idx : k_ok(k) && (idx || b->num_q == 0); }
 bool finite(float x) { return x - x == 0.f; }
 bool rows_q8_ok(const dsa_batch* b) { return b->kv_rows < (int64_t{1} << 31); }   // the kernels keep rows in 32 bits
 
@@ -789,7 +790,8 @@ dsa_status dsa_sparse_mla_q8(const dsa_batch* batch, const uint16_t* q, const ui
   if (!batch_ok(batch) || !ws) return DSA_ERR_INVALID_ARGUMENT;
   if (batch->num_q > 0 && (!q || !kv8 || !scale || !out)) return DSA_ERR_INVALID_ARGUMENT;
   if (!finite(sm_scale)) return DSA_ERR_INVALID_ARGUMENT;
-  if (!h_ok(H) || !k_q8_ok(idx, k) || !block_ok(scale_block) || !paging_ok(batch) || !rows_q8_ok(batch)) return DSA_ERR_UNSUPPORTED;
+  if (!h_ok(H) || !k_q8_ok(batch, idx, k) || !block_ok(scale_block) || !paging_ok(batch) || !rows_q8_ok(batch))
+    return DSA_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(kv8) || !aligned16(out) || !aligned16(ws)) return DSA_ERR_UNSUPPORTED;
   const Q8Layout L = q8_layout(ws, DSA_Q8_MLA, batch, H, k);
   if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;

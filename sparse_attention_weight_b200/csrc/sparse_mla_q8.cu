@@ -74,6 +74,7 @@ struct Q8Smem {
   uint8_t w_lo[kRows * 64];
   float s_row[2][kRows];                           // row scales, 0 = unused row
   float red[kGroups][4][kGH];
+  uint32_t top_s[kGroups][4];                      // largest row scales (bits), beside red
   float qs[kHT];                                   // scale of each head's query
   float m[kHT];                                    // minus the references
   uint64_t rows_full[2], rows_empty[2][4], s_full[2], s_free[2], w_full[4], q_full, q_free, o_full, o_free, l_full, l_free,
@@ -245,7 +246,7 @@ __device__ __forceinline__ void item_list(const MlaQ8Params& p, Item& I) {
   int n = p.k;
   if (!p.idx) {
     const int pos = p.q_pos[I.t];
-    I.ok = I.ok && pos >= 0 && pos < I.len;
+    I.ok = I.ok && pos >= 0 && pos < I.len && pos < static_cast<int64_t>(p.splits) * p.split_tiles * kRows;
     n = pos + 1;
   }
   I.e0 = I.sp * p.split_tiles * kRows;
@@ -400,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
 #pragma unroll
       for (int i = 0; i < kGH; ++i) l[i] = 0.f;
       bool seen = false;                            // a usable row so far
+      float far_s = 0.f;                            // see `far` below
       if (tiles > 0) {
         bad |= !wait(&S.q_full, nq & 1, p.status, ab);
         ++nq;
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         tc_fence_after();
         uint32_t wh[4], wl[4];
         float x[kGH];                               // log2 of the weight, then the weight
-        auto logits = [&]() {
+        auto logits = [&](float add) {
           uint32_t hi[2][8], lo[2][8];
           tmem_ld8(s_at + b * 128, hi[0]);
           tmem_ld8(s_at + b * 128 + kHT, lo[0]);
@@ -437,13 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
                                     make_float2(__uint_as_float(lo[u][i]), __uint_as_float(lo[u][i + 1])));
               // an item's first logits have no reference yet
               const float2 y = ffma2(d, mul2(sc, make_float2(c, c)),
-                                     seen ? add2(make_float2(sg, sg), mm) : make_float2(sg, sg));
+                                     seen ? add2(make_float2(add, add), mm) : make_float2(add, add));
               x[h] = y.x;
               x[h + 1] = y.y;
             }
           }
         };
-        logits();
+        logits(sg);
         auto weights = [&]() {
 #pragma unroll
           for (int i = 0; i < kGH; ++i) x[i] = ex2_approx(x[i]);
@@ -460,15 +462,35 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
           if (nq > 1) bad |= !wait(&S.l_free, nq & 1, p.status, ab);
           __syncwarp();
           if (lane < kGH) S.red[grp][quad][lane] = mine;
+          const uint32_t s_max = __reduce_max_sync(0xffffffffu, __float_as_uint(usable ? s : 0.f));
+          if (lane == 0) S.top_s[grp][quad] = s_max;
           bad |= !meet(&S.sync[grp], met, lane, p.status, ab);
+          const uint32_t(&ts)[4] = S.top_s[grp];
+          far_s = fmaxf(far_s, __uint_as_float(max(max(ts[0], ts[1]), max(ts[2], ts[3]))) * 8.673617e-19f);   // 2^-60
           const int hl = lane & (kGH - 1);
           return fmaxf(fmaxf(S.red[grp][0][hl], S.red[grp][1][hl]), fmaxf(S.red[grp][2][hl], S.red[grp][3][hl]));
+        };
+        // A row whose scale lies 2^60 below that of a row which set a reference: its weight
+        // may be flushed although its share of the denominator (the weight over the scale)
+        // counts, so that the warp works the shares out by themselves.
+        bool far = false;
+        auto shares = [&]() {
+#pragma unroll
+          for (int i = 0; i < kGH; ++i)
+            if (usable) l[i] += ex2_approx(x[i]);
         };
         bool met_now = false;                       // red and m were used: meet again when done
         if (!seen) {
           // set the reference at the first usable rows
           const float mx = largest();
           const float up = fabsf(mx) < INFINITY ? mx - kTop : 0.f;
+          if ((far = __any_sync(0xffffffffu, usable && s < far_s))) {
+            logits(0.f);
+#pragma unroll
+            for (int i = 0; i < kGH; ++i) x[i] -= __shfl_sync(0xffffffffu, up, i);
+            shares();
+            logits(sg);
+          }
           seen = __any_sync(0xffffffffu, mx > -INFINITY);
           if (quad == 0 && lane < kGH) S.m[grp * kGH + lane] = -up;
 #pragma unroll
@@ -493,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
           if ((bad = __any_sync(0xffffffffu, bad))) break;
           if (*const_cast<volatile int*>(&S.over[grp][votes & 1])) {
             // move the reference of the heads that need it
-            logits();
+            logits(sg);
             const float mx = largest();
             const float up = fabsf(mx) < INFINITY && mx > kLimit ? mx - kTop : 0.f;
             const float f = ex2_approx(-up);
@@ -519,8 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
               if (lane == 0) S.over[grp][votes & 1] = 0;
             }
             bad |= !meet(&S.sync[grp], met, lane, p.status, ab);   // m is set, red may be reused
-            logits();
+            logits(sg);
             weights();
+          }
+          if ((far = __any_sync(0xffffffffu, usable && s < far_s))) {
+            logits(0.f);
+            shares();
           }
           ++votes;
         }
@@ -533,11 +559,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.w_full[quad]);
+        if (!far) {
 #pragma unroll
-        for (int i = 0; i < kGH; i += 2) {
-          const float2 y = ffma2(make_float2(x[i], x[i + 1]), make_float2(inv, inv), make_float2(l[i], l[i + 1]));
-          l[i] = y.x;
-          l[i + 1] = y.y;
+          for (int i = 0; i < kGH; i += 2) {
+            const float2 y = ffma2(make_float2(x[i], x[i + 1]), make_float2(inv, inv), make_float2(l[i], l[i + 1]));
+            l[i] = y.x;
+            l[i + 1] = y.y;
+          }
         }
         if (met_now) bad |= !meet(&S.sync[grp], met, lane, p.status, ab);   // m is set, red may be reused
       }

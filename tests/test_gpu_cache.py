@@ -330,6 +330,55 @@ def test_no_queries(cuda_device):
     assert B.read_device_status(ws) == 0
 
 
+def test_no_queries_and_no_pointers(cuda_device):
+    """Empty tensors have no address: an empty batch takes them in either form."""
+    c = Case(23, [20], 1, 8, 4, 1, 0)
+    c.q_seq, c.q_pos = c.q_seq[:0], c.q_pos[:0]
+    db = c.batch(cuda_device)
+    e = torch.empty(0, dtype=torch.uint8, device=cuda_device)
+    for k, idx in ((4, e), (4, None), (0, None)):
+        ws = B.q8_workspace(B.Q8_MLA, db, H=8, k=k, device=cuda_device)
+        B.dsa_sparse_mla_q8(db, e, e, e, 1, idx, k, 8, SM, e, None, ws)
+        assert B.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("top,rest,dense", [(40, -100, False), (40, -100, True), (90, -80, True), (8, -100, False)])
+def test_scales_at_both_ends_in_one_query(cuda_device, top, rest, dense):
+    """Rows of the smallest scale (what the append gives to a block of zeros) beside rows of
+    a large one: they add nothing to the output but their full share to the denominator."""
+    c = Case(28, [900, 2500], 1, 16, 0 if dense else 700, 8, 64)
+    c.scale[:] = 2.0 ** rest
+    for b in range(2):
+        for pos in (1, 160, 500):                        # before, beside and after rows of the small scale
+            c.scale[c.row(b, pos) // 8] = 2.0 ** top
+            if not dense:
+                c.idx[b, pos] = pos
+    sm = SM * 2.0 ** (-top - 6)                          # logits of about 1
+    c.check(*c.run(cuda_device, sm=sm), sm=sm)
+
+
+def test_dense_beyond_the_stated_length(cuda_device):
+    """A position far behind max_kv_len is refused, not answered from part of its rows."""
+    c = Case(29, [900, 100], 1, 16, 0, 8, 64)
+    db = c.batch(cuda_device)
+    db.struct.max_kv_len = 128
+    out, lse = c.run(cuda_device, flags=B.DEV_BAD_QUERY, batch=db)
+    assert (out[0] == 0).all() and (lse[0] == -np.inf).all()
+    c.check(out, lse, rows=[1])
+
+
+@pytest.mark.parametrize("T", [74, 75, 147, 148, 149, 297])
+@pytest.mark.parametrize("H,k", [(72, 300), (16, 0)])
+def test_items_around_the_number_of_sms(cuda_device, T, H, k):
+    r = np.random.default_rng(T)
+    c = Case(T, [int(x) for x in r.integers(1, 400, T)], 1, H, k, 16, 64, holes=0.2 if k else 0.0)
+    if k:
+        c.idx[::5] = -1                                  # items without rows between the others
+        c.check(*c.run(cuda_device), rows=range(0, T, 7))
+    else:
+        c.check(*c.run(cuda_device), rows=range(0, T, 7))
+
+
 def test_results_repeat_bit_for_bit(cuda_device):
     c = Case(24, [3000, 800, 77], 1, 128, 512, 64, 64)
     a, b = c.run(cuda_device), c.run(cuda_device)
@@ -452,6 +501,40 @@ def test_append_long_list(cuda_device):
     codes, scale = _append(cuda_device, c, bits, q_seq, q_pos)
     want = C.quantize_append(c.codes, c.scale, 16, oracle.bf16_decode(bits), q_seq, q_pos, lambda s, p: int(c.row(s, p)))
     assert np.array_equal(scale, want[1].astype(np.float32)) and _same_codes(codes, want[0])
+
+
+@pytest.mark.parametrize("T", [1023, 1024, 1025])
+def test_append_around_the_short_list_rule_captured(cuda_device, T):
+    """Lists at the rule's edge, appended by two captured graphs with a workspace each,
+    replayed one after the other on another stream."""
+    r = np.random.default_rng(T)
+    c = Case(5, [T - 100, 100], 1, 8, 0, 8, 64)
+    q_seq = np.repeat([0, 1], [T - 100, 100])
+    q_pos = np.concatenate([np.arange(T - 100), np.arange(100)])
+    class Host:
+        kv_offset, kv_len = c.off, c.lens
+    Host.q_seq, Host.q_pos = q_seq.astype(np.int32), q_pos.astype(np.int32)
+    db = B.DeviceBatch.from_host(Host, cuda_device, kv_rows=c.rows, page_size=64, page_table=c.table)
+    kv8, scale = B.bits_to_tensor(c.codes, cuda_device), B.bits_to_tensor(c.scale, cuda_device)
+    bits = [inputs.to_bf16_bits(r.standard_normal((T, 576)).astype(np.float32) * f) for f in (4, 1)]
+    kv = [B.bits_to_tensor(x, cuda_device) for x in bits]
+    ws = [B.q8_workspace(B.Q8_APPEND, db, device=cuda_device) for _ in range(2)]
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, x, w in zip(graphs, kv, ws):
+        with torch.cuda.graph(g):
+            B.dsa_quantize_append(db, x, kv8, scale, 8, w)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        for _ in range(3):
+            for g in graphs:
+                g.replay()
+    torch.cuda.synchronize()
+    assert [B.read_device_status(w) for w in ws] == [0, 0]
+    want = c.codes, c.scale
+    for x in bits:
+        want = C.quantize_append(want[0], want[1], 8, oracle.bf16_decode(x), q_seq, q_pos, lambda s, p: int(c.row(s, p)))
+    assert np.array_equal(scale.cpu().numpy(), want[1].astype(np.float32)) and _same_codes(kv8.cpu().numpy(), want[0])
 
 
 def test_append_extreme_values(cuda_device):
