@@ -437,8 +437,8 @@ dsa_status dsa_project_append_q8(const dsa_batch *batch, const uint16_t *hidden,
  * and sums.  A query row with an infinite or NaN entry gives NaN, and so
  * does a selected row with a NaN code.
  * A row whose scale is outside [2^-100, 2^100] raises DSA_DEV_BAD_SCALE and is
- * skipped.  In the dense form a query position outside its sequence raises
- * DSA_DEV_BAD_QUERY; such a query, and one with no usable row, gets out = 0 and
+ * skipped.  In the dense form a query position outside its sequence, or well beyond
+ * max_kv_len, raises DSA_DEV_BAD_QUERY; such a query, and one with no usable row, gets out = 0 and
  * lse = -inf.
  * Workspace: DSA_Q8_MLA.  Supported: H and k as in dsa_sparse_mla; q, kv8, out and
  * ws 16-byte aligned, sm_scale finite.
@@ -472,7 +472,8 @@ typedef struct dsa_page_state {
   int32_t num_seqs;        /* >= 1 */
   int32_t num_pages;       /* >= 1 */
   int32_t page_size;       /* rows per page: a multiple of 64 */
-  int32_t pages_per_seq;   /* >= 1; pages_per_seq * page_size < 2^31 */
+  int32_t pages_per_seq;   /* >= 1; pages_per_seq * page_size < 2^31,
+                            * num_seqs * (pages_per_seq + 1) < 2^31 */
   int32_t *page_table;
   int32_t *seq_len;
   int32_t *ref_count;

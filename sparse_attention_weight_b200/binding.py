@@ -235,7 +235,7 @@ class PageBuffers:
     equal parts, page after page."""
 
     def __init__(self, tensors, num_pages: int):
-        self.tensors = list(tensors)
+        self.tensors, self.num_pages = list(tensors), num_pages
         if len(self.tensors) > MAX_PAGE_BUFFERS:
             raise ValueError(f"at most {MAX_PAGE_BUFFERS} page buffers")
         self.struct = DsaPageBuffers()
@@ -358,7 +358,7 @@ def dsa_forward(batch: DeviceBatch, q_idx, k_idx, w, H_I: int, q, kv, H: int, k:
 def dsa_quantize_append(batch: DeviceBatch, kv, kv8, scale, scale_block: int, ws, stream=None):
     d = torch.cuda.current_device()
     _check("dsa_quantize_append", lib().dsa_quantize_append(
-        ctypes.byref(batch.struct), _dev(kv, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(ws, d), ws.numel(),
+        _batch(batch, d), _dev(kv, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(ws, d), ws.numel(),
         _stream(stream)))
 
 
@@ -366,7 +366,7 @@ def dsa_project_append_q8(batch: DeviceBatch, hidden, w_all, d_model: int, H_I: 
                           w, q, k_idx, kv8, scale, scale_block: int, ws, stream=None):
     d = torch.cuda.current_device()
     _check("dsa_project_append_q8", lib().dsa_project_append_q8(
-        ctypes.byref(batch.struct), _dev(hidden, d), _dev(w_all, d), d_model, H_I, H, rope_base, _dev(q_idx, d), _dev(w, d),
+        _batch(batch, d), _dev(hidden, d), _dev(w_all, d), d_model, H_I, H, rope_base, _dev(q_idx, d), _dev(w, d),
         _dev(q, d), _dev(k_idx, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(ws, d), ws.numel(), _stream(stream)))
 
 
@@ -375,7 +375,7 @@ def dsa_sparse_mla_q8(batch: DeviceBatch, q, kv8, scale, scale_block: int, idx, 
     """Attention over the 8-bit cache; idx = None with k = 0 attends to every visible key."""
     d = torch.cuda.current_device()
     _check("dsa_sparse_mla_q8", lib().dsa_sparse_mla_q8(
-        ctypes.byref(batch.struct), _dev(q, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(idx, d), k, H, sm_scale,
+        _batch(batch, d), _dev(q, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(idx, d), k, H, sm_scale,
         _dev(out, d), _dev(lse, d), _dev(ws, d), ws.numel(), _stream(stream)))
 
 
@@ -383,12 +383,31 @@ def dsa_forward_q8(batch: DeviceBatch, q_idx, k_idx, w, H_I: int, q, kv8, scale,
                    sm_scale: float, out, lse, ws, stream=None):
     d = torch.cuda.current_device()
     _check("dsa_forward_q8", lib().dsa_forward_q8(
-        ctypes.byref(batch.struct), _dev(q_idx, d), _dev(k_idx, d), _dev(w, d), H_I, _dev(q, d), _dev(kv8, d), _dev(scale, d),
+        _batch(batch, d), _dev(q_idx, d), _dev(k_idx, d), _dev(w, d), H_I, _dev(q, d), _dev(kv8, d), _dev(scale, d),
         scale_block, H, k, sm_scale, _dev(out, d), _dev(lse, d), _dev(ws, d), ws.numel(), _stream(stream)))
 
 
-def _buffers(buffers: PageBuffers | None):
-    return ctypes.byref(buffers.struct) if buffers is not None else None
+def _batch(b: DeviceBatch, device: int):
+    """The struct of a batch whose arrays lie on the current device."""
+    if b.q_seq.get_device() != device:
+        raise ValueError("the batch must be on the current CUDA device")
+    return ctypes.byref(b.struct)
+
+
+def _state(s: PageState, device: int):
+    if any(t.get_device() != device for t in (s.page_table, s.seq_len, s.ref_count)):
+        raise ValueError("a page state must be on the current CUDA device")
+    return ctypes.byref(s.struct)
+
+
+def _buffers(buffers: PageBuffers | None, state: PageState, device: int):
+    if buffers is None:
+        return None
+    if buffers.num_pages != state.struct.num_pages:
+        raise ValueError("the page buffers were made for another number of pages")
+    for t in buffers.tensors:
+        _dev(t, device)
+    return ctypes.byref(buffers.struct)
 
 
 def _entries(fn: str, a: torch.Tensor, b: torch.Tensor) -> int:
@@ -402,7 +421,7 @@ def dsa_pages_resize(src: PageState, dst: PageState, seqs, new_len, buffers: Pag
     n = _entries("dsa_pages_resize", seqs, new_len)
     d = torch.cuda.current_device()
     _check("dsa_pages_resize", lib().dsa_pages_resize(
-        ctypes.byref(src.struct), ctypes.byref(dst.struct), n, _dev(seqs, d), _dev(new_len, d), _buffers(buffers),
+        _state(src, d), _state(dst, d), n, _dev(seqs, d), _dev(new_len, d), _buffers(buffers, src, d),
         _dev(ws, d), ws.numel(), _stream(stream)))
 
 
@@ -410,7 +429,7 @@ def dsa_pages_fork(src: PageState, dst: PageState, src_seqs, dst_seqs, ws, strea
     n = _entries("dsa_pages_fork", src_seqs, dst_seqs)
     d = torch.cuda.current_device()
     _check("dsa_pages_fork", lib().dsa_pages_fork(
-        ctypes.byref(src.struct), ctypes.byref(dst.struct), n, _dev(src_seqs, d), _dev(dst_seqs, d), _dev(ws, d), ws.numel(),
+        _state(src, d), _state(dst, d), n, _dev(src_seqs, d), _dev(dst_seqs, d), _dev(ws, d), ws.numel(),
         _stream(stream)))
 
 
@@ -419,7 +438,7 @@ def dsa_pages_compact(src: PageState, dst: PageState, buffers: PageBuffers | Non
     None) receives the new place of each page that was in use."""
     d = torch.cuda.current_device()
     _check("dsa_pages_compact", lib().dsa_pages_compact(
-        ctypes.byref(src.struct), ctypes.byref(dst.struct), _buffers(buffers), _dev(page_map, d), _dev(ws, d), ws.numel(),
+        _state(src, d), _state(dst, d), _buffers(buffers, src, d), _dev(page_map, d), _dev(ws, d), ws.numel(),
         _stream(stream)))
 
 

@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p
       start[i] = need + at;
       p.copies[i] = copy;
     }
-    need = need > INT_MAX - total ? INT_MAX : need + total;
+    need += total;
   }
   // the lowest free pages, four per thread and pass
   int found = 0;
@@ -447,8 +447,11 @@ int sm_count() {
 bool state_ok(const dsa_page_state* s) {
   return s && s->num_seqs >= 1 && s->num_pages >= 1 && s->page_size >= 1 && s->pages_per_seq >= 1;
 }
+// Sums of pages over all sequences, each with a copied page more, stay in 32 bits.
 bool state_supported(const dsa_page_state* s) {
-  return s->page_size % 64 == 0 && static_cast<int64_t>(s->pages_per_seq) * s->page_size < (int64_t{1} << 31);
+  constexpr int64_t most = int64_t{1} << 31;
+  return s->page_size % 64 == 0 && static_cast<int64_t>(s->pages_per_seq) * s->page_size < most &&
+         (static_cast<int64_t>(s->pages_per_seq) + 1) * s->num_seqs < most;
 }
 
 // Workspace: the status word, then the int32 arrays below.

@@ -124,3 +124,47 @@ def test_pages_host_checks(lib):
     assert lib.dsa_pages_fork(ctypes.byref(s), ctypes.byref(o), 2, P, P, WS, 300, None) == 3
     assert lib.dsa_pages_compact(ctypes.byref(s), None, None, None, WS, BIG, None) == 1
     assert lib.dsa_pages_compact(ctypes.byref(s), ctypes.byref(o), bufs((P, 6)), None, WS, BIG, None) == 2
+
+
+def test_page_sums_stay_in_32_bits(lib):
+    big, fits = _state(seqs=1 << 16, pps=1 << 15), _state(seqs=(1 << 16) - 2, pps=1 << 15)
+    assert lib.dsa_pages_workspace_size(ctypes.byref(fits), 1) > 0
+    assert lib.dsa_pages_workspace_size(ctypes.byref(big), 1) == 0
+    assert lib.dsa_pages_resize(ctypes.byref(big), ctypes.byref(big), 1, P, P, None, WS, BIG, None) == 2
+    assert lib.dsa_pages_fork(ctypes.byref(big), ctypes.byref(big), 1, P, P, WS, BIG, None) == 2
+    assert lib.dsa_pages_compact(ctypes.byref(big), ctypes.byref(big), None, None, WS, BIG, None) == 2
+
+
+def test_binding_takes_the_current_device_only(monkeypatch):
+    """Tensors of another device (here: the CPU's, with device 0 current), strided ones and
+    page buffers of another pool size are refused before the library is called."""
+    import numpy as np
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(B, "_stream", lambda s: None)
+
+    class NoCall:
+        def __getattr__(self, name):
+            return lambda *a: pytest.fail(name + " was called")
+    monkeypatch.setattr(B, "lib", lambda: NoCall())
+
+    class Host:
+        kv_offset, kv_len, q_seq, q_pos = np.array([0]), np.array([8]), np.array([0]), np.array([7])
+    b = B.DeviceBatch.from_host(Host, "cpu")
+    x = torch.zeros(64, dtype=torch.int32)
+    s = B.PageState.empty(2, 4, 64, 2, device="cpu")
+    bufs = B.PageBuffers([torch.zeros(8, 4)], 4)
+    calls = [lambda: B.dsa_quantize_append(b, x, x, x, 1, x),
+             lambda: B.dsa_project_append_q8(b, x, x, 8, 4, 8, 1e4, x, x, x, x, x, x, 1, x),
+             lambda: B.dsa_sparse_mla_q8(b, x, x, x, 1, None, 0, 8, 1.0, x, None, x),
+             lambda: B.dsa_forward_q8(b, x, x, x, 4, x, x, x, 1, 8, 4, 1.0, x, None, x),
+             lambda: B.dsa_pages_resize(s, s, x, x, None, x),
+             lambda: B.dsa_pages_fork(s, s, x, x, x),
+             lambda: B.dsa_pages_compact(s, s, None, None, x)]
+    for call in calls:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+    with pytest.raises(ValueError, match="another number of pages"):
+        B._buffers(bufs, B.PageState.empty(2, 8, 64, 2, device="cpu"), -1)
+    with pytest.raises(ValueError, match="contiguous"):
+        B._dev(torch.zeros(4, 4).t()[1:], -1)

@@ -317,3 +317,60 @@ def test_serving_run(cuda_device):
     attend()
     used = int((st.ref_count > 0).sum())
     assert used == len({int(p) for s in range(S) for p in st.page_table[s, :-(-host[s][2] // P)].cpu()})
+
+
+@pytest.mark.parametrize("n", [1023, 1024, 1025])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_lists_around_one_pass(cuda_device, n, in_place):
+    """As many entries as a pass of the planning threads takes, and one more or fewer, with
+    a repeated sequence at the end."""
+    r = np.random.default_rng(n)
+    d = Dev(cuda_device, *_pool(r, 1100, 5000, 64, 4, range(0, 1100, 2), 2500), 64, sizes=(132,), in_place=in_place)
+    seqs = r.permutation(1100)[:n]
+    seqs[-1] = seqs[3]
+    lens = r.integers(0, 2 * 64, n)
+    d.resize(seqs, lens, flags=B.DEV_BAD_QUERY)
+    d.compact()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compaction_of_more_pages_than_shared_memory_has_masks_for(cuda_device, in_place):
+    r = np.random.default_rng(1)
+    N = 131072 + 77
+    d = Dev(cuda_device, *_pool(r, 40, N, 64, 2000, range(40), 60000), 64, sizes=(4, 16), in_place=in_place)
+    d.compact()
+    d.resize(np.arange(0, 40, 3), np.zeros(14, np.int64))
+    d.compact(with_map=False)
+
+
+def test_two_captured_steps_in_place_on_another_stream(cuda_device):
+    """Fork, growth with copies, and compaction of one pool in place, captured as two graphs
+    and replayed on a side stream."""
+    P, S, N, pps = 64, 8, 64, 6
+    r = np.random.default_rng(2)
+    table, lens, refs = _pool(r, S, N, P, pps, range(4), 20)
+    lens[0], table[0, :2] = 100, [60, 61]
+    refs[:] = 0
+    lens[1:4] = 0
+    refs[[60, 61]] = 1
+    d = Dev(cuda_device, table, lens, refs, P, in_place=True)
+    up = lambda x: torch.as_tensor(np.array(x, np.int32), device=cuda_device)  # noqa: E731
+    a, b, c, e = up([0, 0]), up([5, 6]), up([5, 6, 0]), up([130, 101, 128])
+    ws = [B.pages_workspace(d.state, 3, device=cuda_device) for _ in range(3)]
+    torch.cuda.synchronize()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        B.dsa_pages_fork(d.state, d.state, a, b, ws[0])
+        B.dsa_pages_resize(d.state, d.state, c, e, d.buffers, ws[1])
+    with torch.cuda.graph(g2):
+        B.dsa_pages_compact(d.state, d.state, d.buffers, None, ws[2])
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        g1.replay()
+        g2.replay()
+    torch.cuda.synchronize()
+    d.ref.fork([0, 0], [5, 6])
+    d.copied(d.ref.resize([5, 6, 0], [130, 101, 128]))
+    d.copied(d.ref.compact()[1])
+    assert [B.read_device_status(w) for w in ws] == [0, 0, 0]
+    d.check(d.state, ws[2])
