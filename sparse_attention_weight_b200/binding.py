@@ -140,10 +140,10 @@ def _dev(t: torch.Tensor | None, device: int) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device: int | None = None) -> int | None:
     if stream is None:
         # the raw handle: building a Stream object costs more than a small kernel
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     return stream.cuda_stream
 
 
@@ -214,8 +214,12 @@ class PageState:
         if seq_len.numel() != page_table.shape[0]:
             raise ValueError("page_table and seq_len disagree about the number of sequences")
         self.page_table, self.seq_len, self.ref_count = page_table, seq_len, ref_count
+        self.device = page_table.get_device()
+        if seq_len.get_device() != self.device or ref_count.get_device() != self.device:
+            raise ValueError("the arrays of a page state must be on one device")
         self.struct = DsaPageState(page_table.shape[0], ref_count.numel(), page_size, page_table.shape[1],
                                    page_table.data_ptr(), seq_len.data_ptr(), ref_count.data_ptr())
+        self.ref = ctypes.byref(self.struct)
 
     @classmethod
     def empty(cls, num_seqs: int, num_pages: int, page_size: int, pages_per_seq: int, device="cuda") -> "PageState":
@@ -236,6 +240,7 @@ class PageBuffers:
 
     def __init__(self, tensors, num_pages: int):
         self.tensors, self.num_pages = list(tensors), num_pages
+        self.device = self.tensors[0].get_device() if self.tensors else -1
         if len(self.tensors) > MAX_PAGE_BUFFERS:
             raise ValueError(f"at most {MAX_PAGE_BUFFERS} page buffers")
         self.struct = DsaPageBuffers()
@@ -244,8 +249,9 @@ class PageBuffers:
             n = t.numel() * t.element_size()
             if n % num_pages:
                 raise ValueError("a page buffer holds a whole number of bytes per page")
-            self.struct.base[j] = _dev(t, t.get_device())
+            self.struct.base[j] = _dev(t, self.device)
             self.struct.page_bytes[j] = n // num_pages
+        self.ref = ctypes.byref(self.struct)
 
 
 def workspace_size(op: int, batch: DeviceBatch, H_I: int = 64, H: int = 128, k: int = 2048, ld: int = 0) -> int:
@@ -359,7 +365,7 @@ def dsa_quantize_append(batch: DeviceBatch, kv, kv8, scale, scale_block: int, ws
     d = torch.cuda.current_device()
     _check("dsa_quantize_append", lib().dsa_quantize_append(
         _batch(batch, d), _dev(kv, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(ws, d), ws.numel(),
-        _stream(stream)))
+        _stream(stream, d)))
 
 
 def dsa_project_append_q8(batch: DeviceBatch, hidden, w_all, d_model: int, H_I: int, H: int, rope_base: float, q_idx,
@@ -367,7 +373,8 @@ def dsa_project_append_q8(batch: DeviceBatch, hidden, w_all, d_model: int, H_I: 
     d = torch.cuda.current_device()
     _check("dsa_project_append_q8", lib().dsa_project_append_q8(
         _batch(batch, d), _dev(hidden, d), _dev(w_all, d), d_model, H_I, H, rope_base, _dev(q_idx, d), _dev(w, d),
-        _dev(q, d), _dev(k_idx, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(ws, d), ws.numel(), _stream(stream)))
+        _dev(q, d), _dev(k_idx, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(ws, d), ws.numel(),
+        _stream(stream, d)))
 
 
 def dsa_sparse_mla_q8(batch: DeviceBatch, q, kv8, scale, scale_block: int, idx, k: int, H: int, sm_scale: float, out,
@@ -376,7 +383,7 @@ def dsa_sparse_mla_q8(batch: DeviceBatch, q, kv8, scale, scale_block: int, idx, 
     d = torch.cuda.current_device()
     _check("dsa_sparse_mla_q8", lib().dsa_sparse_mla_q8(
         _batch(batch, d), _dev(q, d), _dev(kv8, d), _dev(scale, d), scale_block, _dev(idx, d), k, H, sm_scale,
-        _dev(out, d), _dev(lse, d), _dev(ws, d), ws.numel(), _stream(stream)))
+        _dev(out, d), _dev(lse, d), _dev(ws, d), ws.numel(), _stream(stream, d)))
 
 
 def dsa_forward_q8(batch: DeviceBatch, q_idx, k_idx, w, H_I: int, q, kv8, scale, scale_block: int, H: int, k: int,
@@ -384,7 +391,7 @@ def dsa_forward_q8(batch: DeviceBatch, q_idx, k_idx, w, H_I: int, q, kv8, scale,
     d = torch.cuda.current_device()
     _check("dsa_forward_q8", lib().dsa_forward_q8(
         _batch(batch, d), _dev(q_idx, d), _dev(k_idx, d), _dev(w, d), H_I, _dev(q, d), _dev(kv8, d), _dev(scale, d),
-        scale_block, H, k, sm_scale, _dev(out, d), _dev(lse, d), _dev(ws, d), ws.numel(), _stream(stream)))
+        scale_block, H, k, sm_scale, _dev(out, d), _dev(lse, d), _dev(ws, d), ws.numel(), _stream(stream, d)))
 
 
 def _batch(b: DeviceBatch, device: int):
@@ -395,19 +402,19 @@ def _batch(b: DeviceBatch, device: int):
 
 
 def _state(s: PageState, device: int):
-    if any(t.get_device() != device for t in (s.page_table, s.seq_len, s.ref_count)):
+    if s.device != device:
         raise ValueError("a page state must be on the current CUDA device")
-    return ctypes.byref(s.struct)
+    return s.ref
 
 
 def _buffers(buffers: PageBuffers | None, state: PageState, device: int):
-    if buffers is None:
+    if buffers is None or not buffers.tensors:
         return None
     if buffers.num_pages != state.struct.num_pages:
         raise ValueError("the page buffers were made for another number of pages")
-    for t in buffers.tensors:
-        _dev(t, device)
-    return ctypes.byref(buffers.struct)
+    if buffers.device != device:
+        raise ValueError("page buffers must be on the current CUDA device")
+    return buffers.ref
 
 
 def _entries(fn: str, a: torch.Tensor, b: torch.Tensor) -> int:
@@ -422,7 +429,7 @@ def dsa_pages_resize(src: PageState, dst: PageState, seqs, new_len, buffers: Pag
     d = torch.cuda.current_device()
     _check("dsa_pages_resize", lib().dsa_pages_resize(
         _state(src, d), _state(dst, d), n, _dev(seqs, d), _dev(new_len, d), _buffers(buffers, src, d),
-        _dev(ws, d), ws.numel(), _stream(stream)))
+        _dev(ws, d), ws.numel(), _stream(stream, d)))
 
 
 def dsa_pages_fork(src: PageState, dst: PageState, src_seqs, dst_seqs, ws, stream=None):
@@ -430,7 +437,7 @@ def dsa_pages_fork(src: PageState, dst: PageState, src_seqs, dst_seqs, ws, strea
     d = torch.cuda.current_device()
     _check("dsa_pages_fork", lib().dsa_pages_fork(
         _state(src, d), _state(dst, d), n, _dev(src_seqs, d), _dev(dst_seqs, d), _dev(ws, d), ws.numel(),
-        _stream(stream)))
+        _stream(stream, d)))
 
 
 def dsa_pages_compact(src: PageState, dst: PageState, buffers: PageBuffers | None, page_map, ws, stream=None):
@@ -439,7 +446,7 @@ def dsa_pages_compact(src: PageState, dst: PageState, buffers: PageBuffers | Non
     d = torch.cuda.current_device()
     _check("dsa_pages_compact", lib().dsa_pages_compact(
         _state(src, d), _state(dst, d), _buffers(buffers, src, d), _dev(page_map, d), _dev(ws, d), ws.numel(),
-        _stream(stream)))
+        _stream(stream, d)))
 
 
 def forward_ws_views(batch: DeviceBatch, H_I: int, H: int, k: int, ws) -> tuple[int, int, int]:

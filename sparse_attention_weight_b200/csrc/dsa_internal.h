@@ -200,7 +200,7 @@ struct PagesParams {
   int chunks;                // of one page, over all buffers
   // workspace
   uint32_t* status;
-  int32_t* num_moves;        // [1]
+  int32_t* num_moves;        // [3]: page copies, dropped and taken table entries
   int32_t* first;            // [num_seqs]
   int32_t* sharers;          // [num_pages]
   int32_t* last_sharer;      // [num_pages]
@@ -210,8 +210,10 @@ struct PagesParams {
   int32_t* move_dst;         // [num_pages]
   int32_t* old_len;          // [n]
   int32_t* last_page;        // [n]
-  int32_t* start;            // [n]
-  int32_t* copies;           // [n]
+  int32_t* drop_at;          // [n] prefix sums of the entries' dropped pages
+  int32_t* drop_pos;         // [n] table place of the k-th dropped page, minus k
+  int32_t* take_at;          // [n] the same of the pages taken
+  int32_t* take_pos;         // [n]
 };
 
 // Counts kernel launches made by the library (dsa_launch_count).

@@ -9,6 +9,7 @@
 // with programmatic dependent launch: each is resident, with its lists read, when
 // the one before it ends.  The copies are bound by memory (each byte read and
 // written once): many small chunks in flight per SM.
+#include <atomic>
 #include <climits>
 
 #include "dsa_common.cuh"
@@ -22,6 +23,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kMoveThreads = 128;
 constexpr int kMoveChunk = 8192;                   // bytes of a page that a CTA copies at a time
 constexpr int kSmallPage = 512;                    // pages up to this many bytes are copied by words
+constexpr int kOwnPages = 49152;                   // pages whose counts a resize holds in shared memory
 constexpr int kMaskWords = 4096;                   // pages / 32 whose masks fit in shared memory
 
 // Programmatic dependent launch: let the next kernel of the call in; wait until the
@@ -56,19 +58,30 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
 }
 
 __device__ __forceinline__ int pages_of(int len, int page_size) {
-  return static_cast<int>((static_cast<int64_t>(len) + page_size - 1) / page_size);
+  return len <= 0 ? 0 : static_cast<int>((static_cast<uint32_t>(len) + page_size - 1) / page_size);   // < 2^32
+}
+
+// to = from, four at a time where both are aligned (`i` of `step` threads).
+__device__ __forceinline__ void copy_ints(int32_t* to, const int32_t* from, int64_t n, int64_t i, int64_t step) {
+  int64_t done = 0;
+  if (((reinterpret_cast<uintptr_t>(to) | reinterpret_cast<uintptr_t>(from)) & 15) == 0) {
+    done = n / 4 * 4;
+#pragma unroll 4
+    for (int64_t k = i; k < n / 4; k += step)
+      reinterpret_cast<int4*>(to)[k] = reinterpret_cast<const int4*>(from)[k];
+  }
+  for (int64_t k = done + i; k < n; k += step) to[k] = from[k];
 }
 
 // out = in, for the three arrays of a state; clears the status word.
 __global__ void __launch_bounds__(256) copy_state_kernel(PagesParams p) {
   next_kernel();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-  const int64_t nt = static_cast<int64_t>(p.num_seqs) * p.pages_per_seq;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  for (int64_t i = i0; i < nt; i += step) p.table_out[i] = p.table_in[i];
-  for (int64_t i = i0; i < p.num_seqs; i += step) p.len_out[i] = p.len_in[i];
-  for (int64_t i = i0; i < p.num_pages; i += step) p.ref_out[i] = p.ref_in[i];
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  copy_ints(p.table_out, p.table_in, static_cast<int64_t>(p.num_seqs) * p.pages_per_seq, i, step);
+  copy_ints(p.len_out, p.len_in, p.num_seqs, i, step);
+  copy_ints(p.ref_out, p.ref_in, p.num_pages, i, step);
 }
 
 // The entry that the k-th unit of an exclusive prefix sum `start` [n] belongs to.
@@ -84,26 +97,69 @@ __device__ __forceinline__ int owner_of(const int32_t* start, int n, int k) {
   return lo;
 }
 
-// One CTA works out a resize on the state `out` (which holds the input's values once
-// the kernel before is through) and lists the page copies.  The pages that are
-// dropped and taken are spread over the threads, whichever entries they belong to.
-__global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p, bool clear) {
+// One CTA works out a resize: lengths and reference counts of `out`, which table entries
+// are dropped and filled, and the page copies.  The pages that are dropped and taken are
+// spread over the threads, whichever entries they belong to.  The table's changes are
+// left to the kernel after it (patch_table), so that the grid's other CTAs can copy the
+// table meanwhile.  With kOwn the counts of the pool are worked on in shared memory (a
+// step's thousands of decrements and the search for free pages otherwise take L2's
+// latency each: 256 entries, 24576 pages, 19 us); larger pools have them in `out`, where
+// the kernel before has copied them.
+template <bool kOwn>
+__global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p) {
+  extern __shared__ __align__(16) int32_t own_ref[];   // kOwn: [num_pages]
   __shared__ int sums[32];
   __shared__ int s_moves;
-  __shared__ __align__(16) int s_seq[kPlanThreads];
-  __shared__ int s_start[kPlanThreads];
+  __shared__ int s_seq[kPlanThreads], s_want[kPlanThreads], s_old[kPlanThreads], s_last[kPlanThreads];
+  __shared__ int s_slot[2 * kPlanThreads];         // first a hash table, then two arrays
+  int* const s_at = s_slot;
+  int* const s_pos = s_slot + kPlanThreads;
   const int tid = threadIdx.x;
+  next_kernel();
+  if (blockIdx.x > 0) {
+    copy_ints(p.table_out, p.table_in, static_cast<int64_t>(p.num_seqs) * p.pages_per_seq,
+              static_cast<int64_t>(blockIdx.x - 1) * kPlanThreads + tid,
+              static_cast<int64_t>(gridDim.x - 1) * kPlanThreads);
+    return;
+  }
   const int P = p.page_size, n = p.n;
   const int64_t top = static_cast<int64_t>(p.pages_per_seq) * P;
-  const bool few = n <= kPlanThreads;              // the lists' working copies fit in shared memory
-  int32_t* start = few ? s_start : p.start;
+  int32_t* ref = kOwn ? own_ref : p.ref_out;
+  auto count_of = [&](int pg) { return kOwn ? ref[pg] : __ldcg(&ref[pg]); };
+  // The entries' working copies: in shared memory if a pass of the threads takes them all.
+  const bool few = n <= kPlanThreads;
+  const int32_t* seq = few ? s_seq : p.list_a;
+  const int32_t* want = few ? s_want : p.list_b;
+  int32_t* old_len = few ? s_old : p.old_len;      // -1: not valid
+  int32_t* last_page = few ? s_last : p.last_page; // the partly filled page that an entry grows in, or -1
+  int32_t* at = few ? s_at : p.drop_at;            // prefix sums of the entries' dropped pages
+  int32_t* pos = few ? s_pos : p.drop_pos;         // table place of the k-th dropped page, minus k
   uint32_t flags = 0;
-  next_kernel();
-  if (tid == 0) s_moves = 0;
-  // An entry is valid if it is in range and the first that names its sequence.  The
-  // first places of up to 1024 entries are found by comparing them in shared memory
-  // (one trip less than through `first`).
-  if (!few) {
+  if (tid == 0) {
+    s_moves = 0;
+    if (kOwn) *p.status = 0;
+  }
+  // An entry is valid if it is in range and the first that names its sequence.  Of few
+  // entries the first ones are kept in a hash table in shared memory: a slot belongs to
+  // one sequence and holds the lowest entry that names it.  (Comparing every entry with
+  // those before it took 3.5 us of 256 entries.)
+  auto probe = [&](int s, auto visit) {            // slots of a sequence in turn, until visit says stop
+    for (uint32_t h = static_cast<uint32_t>(s) * 2654435761u >> 21; !visit(&s_slot[h & (2 * kPlanThreads - 1)]); ++h) {
+    }
+  };
+  if (few) {
+    s_seq[tid] = tid < n ? p.list_a[tid] : -1;
+    s_want[tid] = tid < n ? p.list_b[tid] : 0;
+    s_slot[tid] = s_slot[kPlanThreads + tid] = -1;
+    __syncthreads();
+    const int s = s_seq[tid];
+    if (s >= 0)
+      probe(s, [&](int* slot) {
+        const int got = atomicCAS(slot, -1, tid);
+        if (got >= 0 && s_seq[got] == s) atomicMin(slot, tid);
+        return got < 0 || s_seq[got] == s;
+      });
+  } else {
     for (int i = tid; i < n; i += kPlanThreads) {
       const int s = p.list_a[i];
       if (s >= 0 && s < p.num_seqs) p.first[s] = INT_MAX;
@@ -113,34 +169,29 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p
       const int s = p.list_a[i];
       if (s >= 0 && s < p.num_seqs) atomicMin(&p.first[s], i);
     }
-    __syncthreads();
   }
-  s_seq[tid] = few && tid < n ? p.list_a[tid] : -1;
   __syncthreads();
   for (int i = tid; i < n; i += kPlanThreads) {
-    const int s = few ? s_seq[i] : p.list_a[i];
-    const int want = p.list_b[i];
-    bool ok = s >= 0 && s < p.num_seqs && want >= 0 && want <= top;
+    const int s = seq[i], to = want[i];
+    bool ok = s >= 0 && s < p.num_seqs && to >= 0 && to <= top;
     int old = 0;
-    if (ok) {
-      old = p.len_in[s];
-      ok = old >= 0 && old <= top;
-    }
+    if (ok) old = p.len_in[s];
     if (few) {
-      bool again = false;
-      for (int j = 0; j < i; j += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(&s_seq[j]);
-        again |= v.x == s || (v.y == s && j + 1 < i) || (v.z == s && j + 2 < i) || (v.w == s && j + 3 < i);
-      }
-      ok = ok && !again;
+      int first = -1;
+      if (ok)
+        probe(s, [&](const int* slot) {
+          first = *slot;
+          return s_seq[first] == s;
+        });
+      ok = first == i;
     } else {
       ok = ok && __ldcg(&p.first[s]) == i;
     }
-    p.old_len[i] = ok ? old : -1;
+    ok = ok && old >= 0 && old <= top;
+    old_len[i] = ok ? old : -1;
     if (!ok) flags |= DSA_DEV_BAD_QUERY;
-    // growing with a partly filled last page: that page
     int pg = -1;
-    if (ok && want > old && old % P != 0) {
+    if (ok && to > old && old % P != 0) {
       pg = p.table_in[static_cast<int64_t>(s) * p.pages_per_seq + old / P];
       if (pg < 0 || pg >= p.num_pages) {
         flags |= DSA_DEV_BAD_INDEX;
@@ -150,21 +201,28 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p
         p.last_sharer[pg] = -1;
       }
     }
-    p.last_page[i] = pg;
+    last_page[i] = pg;
+  }
+  if (kOwn) {
+    // by the warps without an entry, if they are half of them or more
+    const int first = n <= kPlanThreads / 2 ? (n + 31) / 32 * 32 : 0;
+    if (tid >= first) {
+      copy_ints(own_ref, p.ref_in, p.num_pages, tid - first, kPlanThreads - first);
+      if (p.len_out != p.len_in) copy_ints(p.len_out, p.len_in, p.num_seqs, tid - first, kPlanThreads - first);
+    }
   }
   last_kernel();
-  if (clear && tid == 0) *p.status = 0;
   __syncthreads();
   // the pages behind the new lengths of shrinking entries; who shares a last page
   int dropped = 0;
   for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
     const int i = i0 + tid;
     int drop = 0;
-    if (i < n && p.old_len[i] >= 0) {
-      const int old = p.old_len[i], want = p.list_b[i], pg = p.last_page[i];
-      if (want <= old) {
-        drop = pages_of(old, P) - pages_of(want, P);
-        p.len_out[p.list_a[i]] = want;
+    if (i < n && old_len[i] >= 0) {
+      const int pg = last_page[i];
+      if (want[i] <= old_len[i]) {
+        drop = pages_of(old_len[i], P) - pages_of(want[i], P);
+        p.len_out[seq[i]] = want[i];
       }
       if (pg >= 0) {
         atomicAdd(&p.sharers[pg], 1);
@@ -172,21 +230,27 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p
       }
     }
     int total;
-    const int at = block_scan(drop, sums, total);
-    if (i < n) start[i] = dropped + at;
+    const int before = dropped + block_scan(drop, sums, total);
+    if (i < n) {
+      at[i] = p.drop_at[i] = before;
+      pos[i] = p.drop_pos[i] = drop ? seq[i] * p.pages_per_seq + pages_of(want[i], P) - before : 0;
+    }
     dropped += total;
   }
   __syncthreads();
-  for (int k = tid; k < dropped; k += kPlanThreads) {
-    const int i = owner_of(start, n, k);
-    int32_t* e = p.table_out + static_cast<int64_t>(p.list_a[i]) * p.pages_per_seq + pages_of(p.list_b[i], P) +
-                 (k - start[i]);
-    const int pg = *e;
-    if (pg >= 0 && pg < p.num_pages) {
-      atomicSub(&p.ref_out[pg], 1);
-      *e = -1;
-    } else {
-      flags |= DSA_DEV_BAD_INDEX;
+  for (int64_t k0 = tid; k0 < dropped; k0 += 4 * kPlanThreads) {
+    int pg[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t k = k0 + u * kPlanThreads;
+      pg[u] = k < dropped ? p.table_in[pos[owner_of(at, n, static_cast<int>(k))] + k] : INT_MIN;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (pg[u] >= 0 && pg[u] < p.num_pages)
+        atomicSub(&ref[pg[u]], 1);
+      else if (k0 + u * kPlanThreads < dropped)
+        flags |= DSA_DEV_BAD_INDEX;
     }
   }
   __syncthreads();
@@ -197,69 +261,115 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p
   for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
     const int i = i0 + tid;
     int take = 0, copy = 0;
-    if (i < n && p.list_b[i] > p.old_len[i] && p.old_len[i] >= 0) {
-      const int pg = p.last_page[i];
+    if (i < n && old_len[i] >= 0 && want[i] > old_len[i]) {
+      const int pg = last_page[i];
       if (pg >= 0) {
-        const int r = __ldcg(&p.ref_out[pg]);
+        const int r = count_of(pg);
         copy = r > 1 && !(r <= __ldcg(&p.sharers[pg]) && __ldcg(&p.last_sharer[pg]) == i);
       }
-      take = copy + pages_of(p.list_b[i], P) - pages_of(p.old_len[i], P);
+      take = copy + pages_of(want[i], P) - pages_of(old_len[i], P);
     }
     int total;
-    const int at = block_scan(take, sums, total);
+    const int before = need + block_scan(take, sums, total);
     if (i < n) {
-      start[i] = need + at;
-      p.copies[i] = copy;
+      p.take_at[i] = before;
+      p.take_pos[i] = take ? seq[i] * p.pages_per_seq + pages_of(old_len[i], P) - copy - before : 0;
+      if (!copy) last_page[i] = -1;                // only the pages to be copied are left
     }
     need += total;
   }
-  // the lowest free pages, four per thread and pass
+  __syncthreads();
+  // the lowest free pages, 16 words of 32 per warp and pass; they are taken as they are found
+  constexpr int kWords = 16;
+  const int lane = tid & 31;
   int found = 0;
-  for (int64_t c0 = 0; c0 < p.num_pages && found < need; c0 += 4 * kPlanThreads) {
-    const int64_t pg = c0 + 4 * tid;
-    int is_free[4], mine = 0;
+  for (int64_t c0 = 0; c0 < p.num_pages && found < need; c0 += kWords * kPlanThreads) {
+    const int64_t pg = c0 + (tid >> 5) * (kWords * 32) + lane;
+    bool is_free[kWords];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      is_free[u] = pg + u < p.num_pages && __ldcg(&p.ref_out[pg + u]) == 0;
-      mine += is_free[u];
+    for (int u = 0; u < kWords; ++u)
+      is_free[u] = pg + u * 32 < p.num_pages && count_of(static_cast<int>(pg + u * 32)) == 0;
+    uint32_t mask[kWords];
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < kWords; ++u) {
+      mask[u] = __ballot_sync(0xffffffffu, is_free[u]);
+      mine += __popc(mask[u]);
     }
     int total;
-    int at = found + block_scan(mine, sums, total);
+    int k = found + __shfl_sync(0xffffffffu, block_scan(lane == 0 ? mine : 0, sums, total), 0);
+    if (k < need) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (is_free[u] && at < need) p.free_list[at] = static_cast<int>(pg + u);
-      at += is_free[u];
+      for (int u = 0; u < kWords; ++u) {
+        const int at_k = k + __popc(mask[u] & ((1u << lane) - 1));
+        if ((mask[u] >> lane & 1) && at_k < need) {
+          p.free_list[at_k] = static_cast<int>(pg) + u * 32;
+          ref[pg + u * 32] = 1;
+        }
+        k += __popc(mask[u]);
+      }
     }
     found += total;
   }
   __syncthreads();
-  if (found < need) {
+  if (found < need) {                              // too few: none is taken
     if (tid == 0) set_status(p.status, DSA_DEV_NO_PAGES);
+    for (int k = tid; k < found; k += kPlanThreads) ref[p.free_list[k]] = 0;
+    need = 0;
   } else {
-    for (int i = tid; i < n; i += kPlanThreads)
-      if (p.list_b[i] > p.old_len[i] && p.old_len[i] >= 0) p.len_out[p.list_a[i]] = p.list_b[i];
-    for (int k = tid; k < need; k += kPlanThreads) {
-      const int i = owner_of(start, n, k);
-      int j = k - start[i];                        // first the copy, then the new pages
-      const int to = p.free_list[k];
-      const int have = pages_of(p.old_len[i], P);
-      int32_t* row = p.table_out + static_cast<int64_t>(p.list_a[i]) * p.pages_per_seq;
-      p.ref_out[to] = 1;
-      if (p.copies[i] && j-- == 0) {
-        const int from = p.last_page[i];
+    for (int i = tid; i < n; i += kPlanThreads) {
+      if (!(old_len[i] >= 0 && want[i] > old_len[i])) continue;
+      p.len_out[seq[i]] = want[i];
+      const int from = last_page[i];
+      if (from >= 0) {
         const int m = atomicAdd(&s_moves, 1);
         p.move_src[m] = from;
-        p.move_dst[m] = to;
-        row[have - 1] = to;
-        atomicSub(&p.ref_out[from], 1);
-      } else {
-        row[have + j] = to;
+        p.move_dst[m] = p.free_list[p.take_at[i]];
+        atomicSub(&ref[from], 1);
       }
     }
   }
   if (flags) set_status(p.status, flags);
   __syncthreads();
-  if (tid == 0) *p.num_moves = s_moves;
+  if (kOwn) copy_ints(p.ref_out, own_ref, p.num_pages, tid, kPlanThreads);
+  if (tid == 0) {
+    p.num_moves[0] = s_moves;
+    p.num_moves[1] = dropped;
+    p.num_moves[2] = need;
+  }
+}
+
+// The table's changes of a resize: dropped entries become -1 (those outside the pool are
+// left alone), taken ones get their pages, an entry's copied page first.
+__device__ __forceinline__ void patch_table(const PagesParams& p) {
+  __shared__ int at[2][kPlanThreads], pos[2][kPlanThreads];
+  const int n = p.n;
+  const int count[2] = {__ldcg(&p.num_moves[1]), __ldcg(&p.num_moves[2])};   // dropped, taken
+  if (blockIdx.x * kMoveThreads >= max(count[0], count[1])) return;
+  const bool few = n <= kPlanThreads;              // searched in shared memory
+  if (few) {
+    for (int i = threadIdx.x; i < n; i += kMoveThreads) {
+      at[0][i] = p.drop_at[i];
+      at[1][i] = p.take_at[i];
+      pos[0][i] = p.drop_pos[i];
+      pos[1][i] = p.take_pos[i];
+    }
+    __syncthreads();
+  }
+  for (int what = 0; what < 2; ++what) {
+    const int32_t* a = few ? at[what] : what ? p.take_at : p.drop_at;
+    const int32_t* b = few ? pos[what] : what ? p.take_pos : p.drop_pos;
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; k < count[what];
+         k += static_cast<int64_t>(gridDim.x) * kMoveThreads) {
+      const int64_t e = b[owner_of(a, n, static_cast<int>(k))] + k;
+      if (what) {
+        p.table_out[e] = p.free_list[k];
+      } else {
+        const int pg = p.table_in[e];
+        if (pg >= 0 && pg < p.num_pages) p.table_out[e] = -1;
+      }
+    }
+  }
 }
 
 // A CTA per pair: the pair is checked against the whole list.
@@ -393,9 +503,11 @@ __global__ void __launch_bounds__(256) remap_kernel(PagesParams p) {
 }
 
 // Copies the listed pages in all buffers: large pages chunk by chunk, small ones a
-// run of words over several pages.
+// run of words over several pages.  After a resize also the changes of the table.
+template <bool kPatch>
 __global__ void __launch_bounds__(kMoveThreads) move_pages_kernel(PagesParams p) {
   last_kernel();
+  if (kPatch) patch_table(p);
   const int64_t moves = __ldcg(p.num_moves);
   const int64_t items = moves * p.chunks;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
@@ -437,10 +549,14 @@ __global__ void __launch_bounds__(kMoveThreads) move_pages_kernel(PagesParams p)
   }
 }
 
+// SMs of the current device, asked for once per device (a query costs a third of a launch).
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -476,7 +592,7 @@ PagesParams pages_params(const dsa_page_state* in, const dsa_page_state* out, in
     return x;
   };
   const size_t pages = static_cast<size_t>(in->num_pages);
-  p.num_moves = take(1);
+  p.num_moves = take(3);
   p.first = take(in->num_seqs);
   p.sharers = take(pages);
   p.last_sharer = take(pages);
@@ -486,8 +602,10 @@ PagesParams pages_params(const dsa_page_state* in, const dsa_page_state* out, in
   p.move_dst = take(pages);
   p.old_len = take(n);
   p.last_page = take(n);
-  p.start = take(n);
-  p.copies = take(n);
+  p.drop_at = take(n);
+  p.drop_pos = take(n);
+  p.take_at = take(n);
+  p.take_pos = take(n);
   *bytes = off;
   return p;
 }
@@ -534,10 +652,12 @@ dsa_status take_buffers(const dsa_page_buffers* bufs, PagesParams& p) {
 
 // Launches a kernel of a call; all but the first with programmatic dependent launch.
 template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), int grid, int threads, cudaStream_t st, bool first, Args... args) {
+cudaError_t launch_smem(void (*kernel)(Args...), int grid, int threads, size_t smem, cudaStream_t st, bool first,
+                        Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at = {};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -549,8 +669,27 @@ cudaError_t launch(void (*kernel)(Args...), int grid, int threads, cudaStream_t 
   return e;
 }
 
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), int grid, int threads, cudaStream_t st, bool first, Args... args) {
+  return launch_smem(kernel, grid, threads, 0, st, first, args...);
+}
+
+// The shared memory of a resize that works on the counts there, once per device.
+cudaError_t prepare_own() {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(resize_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(sizeof(int32_t)) * kOwnPages);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 int grid_for(int64_t items) {
-  const int64_t want = (items + 1023) / 1024, most = 8 * sm_count();
+  const int64_t want = (items + 1023) / 1024, most = 8 * static_cast<int64_t>(sm_count());
   return static_cast<int>(want < most ? want : most);
 }
 
@@ -560,10 +699,11 @@ cudaError_t launch_copy_state(const PagesParams& p, cudaStream_t st) {
 }
 
 // Copies of at most `most` pages.
-cudaError_t launch_moves(const PagesParams& p, int64_t most, cudaStream_t st) {
-  if (p.num_bufs == 0) return cudaSuccess;
+cudaError_t launch_moves(const PagesParams& p, int64_t most, bool patch, cudaStream_t st) {
+  if (p.num_bufs == 0 && !patch) return cudaSuccess;
   const int64_t items = most * (p.chunks > 0 ? p.chunks : 1), full = 16 * sm_count();
-  return launch(move_pages_kernel, static_cast<int>(items < full ? items : full), kMoveThreads, st, false, p);
+  return launch(patch ? move_pages_kernel<true> : move_pages_kernel<false>,
+                static_cast<int>(items < full ? items : full), kMoveThreads, st, false, p);
 }
 
 dsa_status status_of(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
@@ -593,9 +733,20 @@ dsa_status dsa_pages_resize(const dsa_page_state* in, const dsa_page_state* out,
   p.list_b = new_len;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool apart = p.table_in != p.table_out;
-  cudaError_t e = apart ? launch_copy_state(p, st) : cudaSuccess;
-  if (e == cudaSuccess) e = launch(resize_plan_kernel, 1, kPlanThreads, st, !apart, p, !apart);
-  if (e == cudaSuccess && n > 0) e = launch_moves(p, n, st);
+  const bool own = p.num_pages <= kOwnPages;
+  if (!own) {
+    cudaError_t e = apart ? launch_copy_state(p, st) : cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st);
+    if (e == cudaSuccess) e = launch(resize_plan_kernel<false>, 1, kPlanThreads, st, !apart, p);
+    if (e == cudaSuccess && n > 0) e = launch_moves(p, n, true, st);
+    return status_of(e);
+  }
+  // the table goes by 8192 entries per CTA, one CTA per SM (they have the plan's shared memory too)
+  const int64_t parts = (static_cast<int64_t>(p.num_seqs) * p.pages_per_seq + 8191) / 8192, most = sm_count() - 1;
+  const int copiers = apart ? static_cast<int>(parts < most ? parts : most) : 0;
+  cudaError_t e = prepare_own();
+  if (e == cudaSuccess)
+    e = launch_smem(resize_plan_kernel<true>, 1 + copiers, kPlanThreads, sizeof(int32_t) * p.num_pages, st, true, p);
+  if (e == cudaSuccess && n > 0) e = launch_moves(p, n, true, st);
   return status_of(e);
 }
 
@@ -624,7 +775,7 @@ dsa_status dsa_pages_compact(const dsa_page_state* in, const dsa_page_state* out
   cudaError_t e = launch(compact_plan_kernel, 1, kPlanThreads, st, true, p);
   if (e == cudaSuccess)
     e = launch(remap_kernel, grid_for(static_cast<int64_t>(p.num_seqs) * p.pages_per_seq), 256, st, false, p);
-  if (e == cudaSuccess) e = launch_moves(p, p.num_pages, st);
+  if (e == cudaSuccess) e = launch_moves(p, p.num_pages, false, st);
   return status_of(e);
 }
 

@@ -19,6 +19,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 
@@ -247,12 +249,24 @@ __global__ void __launch_bounds__(kQuantThreads, kCtasPerSm) quantize_append_ker
 
 }  // namespace
 
+// The kernel's shared memory, once per device.
+static cudaError_t prepare_device(size_t smem) {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(quantize_append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 cudaError_t launch_quantize_append(const QuantParams& params, int sms, cudaStream_t stream) {
   if (params.T == 0) return cudaSuccess;
   QuantParams p = params;
   const size_t smem = sizeof(QuantSmem);
-  cudaError_t e =
-      cudaFuncSetAttribute(quantize_append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = prepare_device(smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;

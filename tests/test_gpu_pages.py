@@ -374,3 +374,31 @@ def test_two_captured_steps_in_place_on_another_stream(cuda_device):
     d.copied(d.ref.compact()[1])
     assert [B.read_device_status(w) for w in ws] == [0, 0, 0]
     d.check(d.state, ws[2])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("N", [49152, 49153, 120001])
+def test_resize_of_pools_around_what_shared_memory_holds(cuda_device, N, in_place):
+    r = np.random.default_rng(N)
+    S, P, pps = 300, 64, 700
+    d = Dev(cuda_device, *_pool(r, S, N, P, pps, range(0, S, 2), N // 2), P, sizes=(4, 132), in_place=in_place)
+    d.fork(np.arange(0, 20, 2), np.arange(1, 21, 2))
+    for _ in range(4):
+        n = int(r.integers(1, S))
+        seqs = r.permutation(S)[:n]
+        now = d.ref.lens[seqs].astype(np.int64)
+        lens = np.where(r.random(n) < 0.4, r.integers(0, now + 1), np.minimum(now + r.integers(0, 3000, n), pps * P))
+        probe = C.Pool(d.ref.table, d.ref.lens, d.ref.refs, P)
+        probe.resize(seqs, lens)
+        d.resize(seqs, lens, flags=B.DEV_NO_PAGES if probe.no_pages else 0)
+
+
+def test_sequences_that_meet_in_the_hash_table(cuda_device):
+    """Many entries of few sequences, sequences far apart, and every sequence twice."""
+    r = np.random.default_rng(5)
+    S = 200000
+    d = Dev(cuda_device, np.full((S, 1), -1, np.int32), np.zeros(S, np.int32), np.zeros(3000, np.int32), 64, sizes=(4,))
+    seqs = (np.arange(1024, dtype=np.int64) * 2048 * 97) % S
+    seqs = np.concatenate([np.unique(seqs)[:500], np.unique(seqs)[:500], [7] * 24])
+    d.resize(r.permutation(seqs), r.integers(0, 65, seqs.size), flags=B.DEV_BAD_QUERY)
+    d.resize(np.arange(1024) * 190, r.integers(0, 65, 1024))
