@@ -462,10 +462,10 @@ dsa_status run_quantize(const dsa_batch* b, const uint16_t* kv, uint8_t* kv8, fl
   return cuda_status(launch_quantize_append(p, num_sms(), st));
 }
 
-// The status word and the item counter after it are 0.
+// The status word and the item counter after it are 0, or cleared first.
 dsa_status run_mla_q8(const dsa_batch* b, const uint16_t* q, const uint8_t* kv8, const float* scale, int block,
                       const int32_t* idx, int k, int H, float sm_scale, uint16_t* out, float* lse, const Q8Layout& L,
-                      cudaStream_t st) {
+                      bool clear, cudaStream_t st) {
   MlaQ8Params p{};
   p.q = q;
   p.kv8 = kv8;
@@ -493,7 +493,7 @@ dsa_status run_mla_q8(const dsa_batch* b, const uint16_t* q, const uint8_t* kv8,
   p.counter = reinterpret_cast<int32_t*>(L.status + 1);
   p.part_o = L.part_o;
   p.part_lse = L.part_lse;
-  return cuda_status(launch_sparse_mla_q8(p, num_sms(), st));
+  return cuda_status(launch_sparse_mla_q8(p, clear, num_sms(), st));
 }
 
 }  // namespace
@@ -795,9 +795,8 @@ dsa_status dsa_sparse_mla_q8(const dsa_batch* batch, const uint16_t* q, const ui
   if (!aligned16(q) || !aligned16(kv8) || !aligned16(out) || !aligned16(ws)) return DSA_ERR_UNSUPPORTED;
   const Q8Layout L = q8_layout(ws, DSA_Q8_MLA, batch, H, k);
   if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(L.status, 0, 2 * sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
-  return run_mla_q8(batch, q, kv8, scale, scale_block, idx, k, H, sm_scale, out, lse, L, st);
+  return run_mla_q8(batch, q, kv8, scale, scale_block, idx, k, H, sm_scale, out, lse, L, true,
+                    static_cast<cudaStream_t>(stream));
 }
 
 dsa_status dsa_forward_q8(const dsa_batch* batch, const uint8_t* q_idx, const uint8_t* k_idx, const float* w, int H_I,
@@ -820,7 +819,7 @@ dsa_status dsa_forward_q8(const dsa_batch* batch, const uint8_t* q_idx, const ui
   if (s != DSA_OK) return s;
   s = run_topk(batch, L.fwd.scores, ld, k, L.fwd.idx, L.fwd, st);
   if (s != DSA_OK) return s;
-  return run_mla_q8(batch, q, kv8, scale, scale_block, L.fwd.idx, k, H, sm_scale, out, lse, L, st);
+  return run_mla_q8(batch, q, kv8, scale, scale_block, L.fwd.idx, k, H, sm_scale, out, lse, L, false, st);
 }
 
 dsa_status dsa_forward_ws_views(const dsa_batch* batch, int H_I, int H, int k, void* ws, float** scores, int64_t* ld,

@@ -179,7 +179,8 @@ struct MlaQ8Params {
 };
 // Parts that each query's row list is cut into, and the 128-row tiles of a part.
 int mla_q8_plan(int T, int H, int64_t most, int64_t mean, int sms, int* split_tiles);
-cudaError_t launch_sparse_mla_q8(const MlaQ8Params& p, int sms, cudaStream_t stream);
+// clear: the status word and the counter (beside one another) are cleared first.
+cudaError_t launch_sparse_mla_q8(const MlaQ8Params& p, bool clear, int sms, cudaStream_t stream);
 
 struct PagesParams {
   int num_seqs, num_pages, page_size, pages_per_seq;
