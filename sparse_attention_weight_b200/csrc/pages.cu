@@ -480,9 +480,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesParams 
   if (tid == 0) *p.num_moves = moves;
 }
 
-__global__ void __launch_bounds__(256) remap_kernel(PagesParams p) {
-  next_kernel();
-  last_kernel();
+// The table's changes of a compaction: entries in use follow the map; the rest is copied.
+__device__ __forceinline__ void remap_table(const PagesParams& p) {
   const int64_t nt = static_cast<int64_t>(p.num_seqs) * p.pages_per_seq;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -503,11 +502,15 @@ __global__ void __launch_bounds__(256) remap_kernel(PagesParams p) {
 }
 
 // Copies the listed pages in all buffers: large pages chunk by chunk, small ones a
-// run of words over several pages.  After a resize also the changes of the table.
-template <bool kPatch>
+// run of words over several pages.  Before that the changes of the table, of a resize or
+// a compaction.
+template <bool kResize>
 __global__ void __launch_bounds__(kMoveThreads) move_pages_kernel(PagesParams p) {
   last_kernel();
-  if (kPatch) patch_table(p);
+  if (kResize)
+    patch_table(p);
+  else
+    remap_table(p);
   const int64_t moves = __ldcg(p.num_moves);
   const int64_t items = moves * p.chunks;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
@@ -698,12 +701,13 @@ cudaError_t launch_copy_state(const PagesParams& p, cudaStream_t st) {
                 true, p);
 }
 
-// Copies of at most `most` pages.
-cudaError_t launch_moves(const PagesParams& p, int64_t most, bool patch, cudaStream_t st) {
-  if (p.num_bufs == 0 && !patch) return cudaSuccess;
-  const int64_t items = most * (p.chunks > 0 ? p.chunks : 1), full = 16 * sm_count();
-  return launch(patch ? move_pages_kernel<true> : move_pages_kernel<false>,
-                static_cast<int>(items < full ? items : full), kMoveThreads, st, false, p);
+// The table's changes and copies of at most `most` pages.
+template <bool kResize>
+cudaError_t launch_moves(const PagesParams& p, int64_t most, cudaStream_t st) {
+  const int64_t entries = kResize ? 0 : static_cast<int64_t>(p.num_seqs) * p.pages_per_seq / kMoveThreads + 1;
+  const int64_t copies = p.num_bufs > 0 ? most * (p.chunks > 0 ? p.chunks : 1) : kResize ? most : 0;
+  const int64_t items = copies > entries ? copies : entries, full = 16 * static_cast<int64_t>(sm_count());
+  return launch(move_pages_kernel<kResize>, static_cast<int>(items < full ? items : full), kMoveThreads, st, false, p);
 }
 
 dsa_status status_of(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
@@ -737,7 +741,7 @@ dsa_status dsa_pages_resize(const dsa_page_state* in, const dsa_page_state* out,
   if (!own) {
     cudaError_t e = apart ? launch_copy_state(p, st) : cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st);
     if (e == cudaSuccess) e = launch(resize_plan_kernel<false>, 1, kPlanThreads, st, !apart, p);
-    if (e == cudaSuccess && n > 0) e = launch_moves(p, n, true, st);
+    if (e == cudaSuccess && n > 0) e = launch_moves<true>(p, n, st);
     return status_of(e);
   }
   // the table goes by 8192 entries per CTA, one CTA per SM (they have the plan's shared memory too)
@@ -746,7 +750,7 @@ dsa_status dsa_pages_resize(const dsa_page_state* in, const dsa_page_state* out,
   cudaError_t e = prepare_own();
   if (e == cudaSuccess)
     e = launch_smem(resize_plan_kernel<true>, 1 + copiers, kPlanThreads, sizeof(int32_t) * p.num_pages, st, true, p);
-  if (e == cudaSuccess && n > 0) e = launch_moves(p, n, true, st);
+  if (e == cudaSuccess && n > 0) e = launch_moves<true>(p, n, st);
   return status_of(e);
 }
 
@@ -773,9 +777,7 @@ dsa_status dsa_pages_compact(const dsa_page_state* in, const dsa_page_state* out
   if (page_map) p.map = page_map;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch(compact_plan_kernel, 1, kPlanThreads, st, true, p);
-  if (e == cudaSuccess)
-    e = launch(remap_kernel, grid_for(static_cast<int64_t>(p.num_seqs) * p.pages_per_seq), 256, st, false, p);
-  if (e == cudaSuccess) e = launch_moves(p, p.num_pages, false, st);
+  if (e == cudaSuccess) e = launch_moves<false>(p, p.num_pages, st);
   return status_of(e);
 }
 
