@@ -388,7 +388,9 @@ int log2_of(int g) {
   return l;
 }
 // The sparse form has a list, the dense one k = 0; an empty batch may have no pointers.
-bool k_q8_ok(const dsa_batch* b, const int32_t* idx, int k) { return k == 0 ? !idx : k_ok(k) && (idx || b->num_q == 0); }
+bool k_q8_ok(const dsa_batch* b, const int32_t* idx, int k) {
+  return k == 0 ? !idx : k_ok(k) && (idx || b->num_q == 0);
+}
 bool finite(float x) { return x - x == 0.f; }
 bool rows_q8_ok(const dsa_batch* b) { return b->kv_rows < (int64_t{1} << 31); }   // the kernels keep rows in 32 bits
 
@@ -779,7 +781,8 @@ dsa_status dsa_project_append_q8(const dsa_batch* batch, const uint16_t* hidden,
   if (ws_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(L.status, 0, 2 * sizeof(uint32_t), st) != cudaSuccess) return DSA_ERR_CUDA;
-  const dsa_status s = run_project(batch, hidden, w_all, d_model, H_I, H, rope_base, q_idx, w, q, k_idx, nullptr, L, st);
+  const dsa_status s =
+      run_project(batch, hidden, w_all, d_model, H_I, H, rope_base, q_idx, w, q, k_idx, nullptr, L, st);
   if (s != DSA_OK) return s;
   return run_quantize(batch, L.kv_new, kv8, scale, scale_block, L.status, L.runs, st);
 }

