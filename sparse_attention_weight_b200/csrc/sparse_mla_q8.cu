@@ -1010,7 +1010,8 @@ __global__ void __launch_bounds__(128) combine_kernel(MlaQ8Params p) {
     if (!kEager) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        o[i] = load_if(p.part_o + (at + static_cast<int64_t>(s0 + i) * p.H) * DSA_D_V + tid * 4, w[i] != 0.f);
+        o[i] = load_if(p.part_o + (at + static_cast<int64_t>(s0 + i) * p.H) * DSA_D_V + tid * 4,
+                       s0 + i < p.splits && w[i] != 0.f);   // with a NaN among the parts every weight is NaN
     } else if (s0 > 0) {
       load(s0);
     }

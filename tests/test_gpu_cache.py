@@ -286,6 +286,28 @@ def test_nan_and_infinity_stay_where_they_are(cuda_device):
     assert np.array_equal(out[~want], ref[0][~want])
 
 
+@pytest.mark.parametrize("T,H", [(1, 128), (10, 128), (20, 64)])
+@pytest.mark.parametrize("dense", [False, True])
+def test_nan_in_a_part_of_a_split_list(cuda_device, T, H, dense):
+    """A NaN row makes its query NaN, whichever part of the list it lies in (the last query
+    too, behind whose parts nothing is), and no other query; an empty part stays out of it."""
+    lens = [2300 + 64 * t for t in range(T)]
+    c = Case(30 + T, lens, 1, H, 0 if dense else 2048, 64, 64)
+    if not dense and T > 1:
+        c.idx[1] = -1
+        c.idx[1, :300] = np.arange(300)                  # later parts empty
+    want = c.run(cuda_device)
+    for t in {0, T // 2, T - 1}:
+        pos = 1234 if dense else int(c.idx[t][c.idx[t] >= 0][-1])
+        c.codes[c.row(t, np.array([pos]))] = 0x7F
+    out, lse = c.run(cuda_device)
+    hit = np.zeros(T, bool)
+    hit[[0, T // 2, T - 1]] = True
+    nan = np.isnan(oracle.bf16_decode(out))
+    assert nan[hit].all() and np.isnan(lse[hit]).all() and not nan[~hit].any()
+    assert np.array_equal(out[~hit], want[0][~hit]) and np.array_equal(lse[~hit], want[1][~hit])
+
+
 def test_flags(cuda_device):
     c = Case(20, [200, 150, 90], 1, 16, 60, 8, 64)
     good = c.idx.copy()
