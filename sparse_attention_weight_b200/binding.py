@@ -196,6 +196,8 @@ class DeviceBatch:
         for t in (q_seq, q_pos):
             if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != q_seq.numel():
                 raise ValueError("q_seq and q_pos must be contiguous int32 tensors of one length")
+            if t.get_device() != state.device:
+                raise ValueError("q_seq and q_pos must be on the page state's device")
         st = DsaBatch(state.struct.num_seqs, q_seq.numel(), max_kv_len, max_q_per_seq,
                       state.struct.num_pages * state.struct.page_size, None, state.seq_len.data_ptr(),
                       q_seq.data_ptr(), q_pos.data_ptr(), state.struct.page_size, state.struct.pages_per_seq,

@@ -168,3 +168,20 @@ def test_binding_takes_the_current_device_only(monkeypatch):
         B._buffers(bufs, B.PageState.empty(2, 8, 64, 2, device="cpu"), -1)
     with pytest.raises(ValueError, match="contiguous"):
         B._dev(torch.zeros(4, 4).t()[1:], -1)
+
+
+def test_batches_and_states_of_mixed_devices_are_refused():
+    import torch
+    lists = [torch.zeros(2, dtype=torch.int32) for _ in range(2)]
+    on_cpu = B.PageState.empty(2, 4, 64, 2, device="cpu")
+    assert B.DeviceBatch.from_pages(on_cpu, *lists, 128).struct.kv_rows == 256
+    on_cpu.device = 0                                    # as if its arrays lay on a GPU
+    with pytest.raises(ValueError, match="page state's device"):
+        B.DeviceBatch.from_pages(on_cpu, *lists, 128)
+    meta = torch.zeros(2, dtype=torch.int32, device="meta")
+    meta.get_device = lambda: 0
+    with pytest.raises(ValueError, match="one device"):
+        B.PageState(torch.zeros(2, 2, dtype=torch.int32), meta, torch.zeros(4, dtype=torch.int32), 64)
+    on_cpu.device = -1
+    with pytest.raises(ValueError, match="one length"):
+        B.DeviceBatch.from_pages(on_cpu, lists[0], lists[1][:1], 128)
