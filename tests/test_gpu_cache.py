@@ -559,6 +559,41 @@ def test_append_around_the_short_list_rule_captured(cuda_device, T):
     assert np.array_equal(scale.cpu().numpy(), want[1].astype(np.float32)) and _same_codes(kv8.cpu().numpy(), want[0])
 
 
+@pytest.mark.parametrize("T", [2047, 2048, 2049, 9000])
+def test_append_on_both_sides_of_the_search_for_runs(cuda_device, T):
+    test_append_around_the_short_list_rule_captured(cuda_device, T)
+
+
+@pytest.mark.parametrize("page", [0, 64])
+@pytest.mark.parametrize("g", [1, 64])
+def test_append_many_short_runs(cuda_device, g, page):
+    """A long list of one to three tokens per sequence, more runs than CTAs, among them
+    runs that are refused (no page, a sequence too short) and ones that raise a scale."""
+    r = np.random.default_rng(g)
+    n = 1500
+    old, new = r.integers(0, 130, n), r.integers(1, 4, n)
+    c = Case(6, [int(x) for x in old + new], 1, 8, 0, g, page)
+    q_seq = np.repeat(np.arange(n), new)
+    q_pos = np.concatenate([np.arange(o, o + k) for o, k in zip(old, new)])
+    assert q_seq.size > 2048
+    bits = inputs.to_bf16_bits(r.standard_normal((q_seq.size, 576)).astype(np.float32)
+                               * np.exp2(r.integers(-6, 6, (q_seq.size, 1))).astype(np.float32))
+    bad, flags = np.zeros(n, bool), 0
+    c.lens = c.lens.copy()
+    c.lens[[5, 700]] = old[[5, 700]]
+    bad[[5, 700]], flags = True, B.DEV_BAD_QUERY
+    if page:
+        c.table[[9, 901], (old // 64)[[9, 901]]] = -1
+        whole = old // 64 == (old + new - 1) // 64
+        assert whole[[9, 901]].all()
+        bad[[9, 901]], flags = True, flags | B.DEV_BAD_INDEX
+    codes, scale = _append(cuda_device, c, bits, q_seq, q_pos, flags=flags)
+    keep = ~bad[q_seq]
+    want = C.quantize_append(c.codes, c.scale, g, oracle.bf16_decode(bits[keep]), q_seq[keep], q_pos[keep],
+                             lambda s, p: int(c.row(s, p)))
+    assert np.array_equal(scale, want[1].astype(np.float32)) and _same_codes(codes, want[0])
+
+
 def test_append_extreme_values(cuda_device):
     c = Case(4, [64 * 9], 1, 8, 0, 64, 0)
     kv = np.zeros((64 * 9, 576), np.float32)
