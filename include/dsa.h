@@ -431,10 +431,14 @@ dsa_status dsa_project_append_q8(const dsa_batch *batch, const uint16_t *hidden,
  *       form, every visible key 0 .. q_pos[t] of any context length
  * The cache's codes are the tensor cores' operand as they are; the bf16 queries and
  * the softmax weights (times their rows' scales) enter as sums of two E4M3 numbers,
- * which hold 8 significant bits like bf16, down to an absolute error of 2^-15 of the
- * largest p_i * scale_i of the query and head (weights) and of 2^-17 of the
- * largest entry of the query's head (queries).  fp32 logits, softmax statistics
- * and sums.  A query row with an infinite or NaN entry gives NaN, and so
+ * which hold 8 significant bits like bf16 down to 2^-8 of the largest entry of the
+ * query's head (queries; an absolute error of 2^-17 of that entry below) and to 2^-7 of
+ * the largest p_i * scale_i (weights; steps of 2^-14 of it below).  A weight smaller than
+ * its step is taken up to the step or down to 0 by an offset that goes by its place in
+ * the list, evenly spread, so that the sum over many small weights keeps its value: its
+ * deviation is at most 2^-8.6 of the values' root mean square, whatever the number of
+ * rows (bf16 weights: 2^-9 of each).  The results depend on the inputs alone.  fp32
+ * logits, softmax statistics and sums.  A query row with an infinite or NaN entry gives NaN, and so
  * does a selected row with a NaN code.
  * A row whose scale is outside [2^-100, 2^100] raises DSA_DEV_BAD_SCALE and is
  * skipped.  In the dense form a query position outside its sequence, or well beyond

@@ -1,0 +1,110 @@
+"""The 8-bit cache over the range of its inputs, on lists that are not cut into parts: one
+CTA then goes through all tiles of a list, with the reference of its weights running
+(shorter batches are cut into parts of a tile, which the combine joins).
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from sparse_attention_weight_b200 import binding as B
+from sparse_attention_weight_b200 import build, inputs
+from tests.test_gpu_cache import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    B.lib()
+
+
+class Whole(Case):
+    """One sequence of n rows and as many equal queries at its end as keep the lists whole:
+    at least one per SM."""
+
+    def __init__(self, seed, n, H, dense, g=64, page=64):
+        super().__init__(seed, [n], 1, H, 0, g, page)
+        T = torch.cuda.get_device_properties(0).multi_processor_count + 1
+        self.k = 0 if dense else n
+        self.T = T
+        self.q_seq, self.q_pos = np.zeros(T, np.int32), np.full(T, n - 1, np.int32)
+        self.idx = None if dense else np.tile(np.arange(n, dtype=np.int32), (T, 1))
+        self.q = np.repeat(self.q, T, 0)
+
+    def run(self, dev, **kw):
+        db = kw.get("batch") or self.batch(dev)
+        assert B.q8_workspace(B.Q8_MLA, db, H=self.H, k=self.k, device=dev).numel() == 256   # no parts
+        return super().run(dev, **kw)
+
+
+# ------------------------------------------------------------------- a sink and thousands of small weights
+@pytest.mark.parametrize("n,dense", [(2048, False), (2048, True), (8191, True), (32768, True)])
+@pytest.mark.parametrize("where", ["first", "last", "middle"])
+def test_small_weights_beside_a_sink(cuda_device, n, dense, where):
+    """One row holds 0.5 to 0.95 of the weight, the others (unit-normal logits, values of
+    mean 1 and variance 1) the rest, each too small to be held by itself.
+
+    Tolerance: 3e-3 of the norm of a head's output, whatever the length.  The sink is held
+    at 2^7 or more (it is at least the sum of the others, which the reference puts there),
+    and small weights in steps of 2^-9, u = 2^-16 of the sink, rounded up or down in the
+    proportion that keeps their mean, so that a weight w (the sink 1) has a variance of at
+    most u w and the sum over all of them, (1 - p) / p, one of u (1 - p) / p.
+    Divided by the sum of the weights, 1 / p, that is a deviation of sqrt(u p (1 - p)) <=
+    2^-9 of the values' size sqrt(2), against an output of at least sqrt(1 + p^2) per dim:
+    2.5e-3 at p = 0.5.  The bf16 output adds 2^-8 / sqrt(3) of a mantissa's mean square,
+    1.7e-3, independently: 3.0e-3 together.
+    """
+    H = 16
+    c = Whole(40 + n, n, H, dense)
+    r = np.random.default_rng(n)
+    sink = {"first": 0, "last": n - 1, "middle": n // 2}[where]
+    rows = np.zeros((n, 576))
+    rows[:, :512] = r.standard_normal((n, 512)) + 1
+    rows[:, 512:575] = r.standard_normal((n, 63))
+    rows[sink, 512:575] = 0
+    rows[sink, 575] = 16
+    c.codes[c.row(0, np.arange(n))] = inputs.to_e4m3_bytes(rows.astype(np.float32))
+    c.scale[:] = 1.0
+    sm = 1 / np.sqrt(63)
+    v = oracle.e4m3_decode(c.codes[c.row(0, np.arange(n))])
+    q = np.zeros((H, 576))
+    q[:, 512:575] = oracle.bf16_decode(inputs.to_bf16_bits(r.standard_normal((H, 63)).astype(np.float32)))
+    z = sm * (q @ v.T)
+    z[:, sink] = -np.inf
+    want = np.array([0.5, 0.8, 0.9, 0.95])[np.arange(H) % 4]
+    q[:, 575] = (np.log(np.exp(z).sum(1)) + np.log(want / (1 - want))) / (sm * 16)
+    c.q = np.repeat(inputs.to_bf16_bits(q.astype(np.float32))[None], c.T, 0)
+    out, lse = c.run(cuda_device, sm=sm)
+    assert (out == out[0]).all() and (lse == lse[0]).all()
+    got, q = oracle.bf16_decode(out[0]), oracle.bf16_decode(c.q[0])
+    ref, ref_lse = oracle.sparse_mla(q[None], v, np.arange(n)[None], sm)
+    p = np.exp(sm * (q @ v[sink]) - ref_lse[0])
+    assert (p > 0.4).all() and (p < 0.97).all()
+    err = np.linalg.norm(got - ref[0], axis=1) / np.linalg.norm(ref[0], axis=1)
+    print(f"sink {where} of {n}: " + " ".join(f"{x * 1e3:.2f}" for x in err))
+    assert (err <= 3e-3).all()
+    assert (np.abs(lse[0] - ref_lse[0]) <= 1e-3).all()
+
+
+# ------------------------------------------------------------------- the running reference
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("order", ["rising", "falling", "both"])
+def test_growing_logits_of_a_whole_list(cuda_device, order, dense):
+    """Logits that rise, fall, or rise and fall by far more than a factor of 2^8 per tile."""
+    n, H = 2000, 16
+    c = Whole(60, n, H, dense)
+    at = {"rising": np.arange(n), "falling": np.arange(n)[::-1],
+          "both": np.where(np.arange(n) < n // 2, np.arange(n), n - np.arange(n)) * 2}[order]
+    rows = np.zeros((n, 576))
+    rows[:, :512] = np.random.default_rng(2).standard_normal((n, 512))
+    rows[:, 575] = at / 40.0
+    c.codes[c.row(0, np.arange(n))] = inputs.to_e4m3_bytes(rows.astype(np.float32))
+    c.scale[:] = 1.0
+    q = np.random.default_rng(3).standard_normal((H, 576)).astype(np.float32)
+    q[:, 575] = np.linspace(1, 200, H)
+    c.q = np.repeat(inputs.to_bf16_bits(q)[None], c.T, 0)
+    c.check(*c.run(cuda_device), rows=[0, c.T - 1])
