@@ -580,7 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
             logits(sg);
             const float mx = top_sum();
             const float up = fabsf(mx) < INFINITY && mx > kTop ? mx - kTop : 0.f;
-            const float f = ex2_approx(-up);
+            // The factor may lie below fp32's range: O, relative to the new weights, is then
+            // nothing, but rows of far smaller scales count in l (w / s), which takes it in halves.
+            const float half = ex2_approx(-0.5f * up), f = half * half;
             // O so far: wait for the product of the tile before this one
             bad |= !wait(&S.rows_empty[b ^ 1][3], ((g - 1) >> 1) & 1, p.status, ab);
             __syncwarp();
@@ -597,7 +599,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
             }
             tmem_st_wait();
 #pragma unroll
-            for (int i = 0; i < kGH; ++i) l[i] *= __shfl_sync(0xffffffffu, f, i);
+            for (int i = 0; i < kGH; ++i) {
+              const float h = __shfl_sync(0xffffffffu, half, i);
+              l[i] = l[i] * h * h;
+            }
             if (quad == 0) {
               if (lane < kGH) S.m[grp * kGH + lane] -= up;
               if (lane == 0) S.over[grp][votes & 1] = 0;

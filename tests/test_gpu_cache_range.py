@@ -92,6 +92,22 @@ def test_small_weights_beside_a_sink(cuda_device, n, dense, where):
 
 # ------------------------------------------------------------------- the running reference
 @pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("tops", [(-100, 40), (-100, 20, 60, 90), (40, -100), (40, -100, 40), (-100, 40, -100, 90),
+                                  (-60, 70), (0, 0, 100, -100)], ids=str)
+def test_scales_from_end_to_end_of_a_whole_list(cuda_device, tops, dense):
+    """Runs of one to three tiles whose scales lie 2^100 and more apart, in rising, falling
+    and mixed order: the reference moves by more than fp32's exponents, and every row keeps
+    its share of the denominator."""
+    n = 1024
+    c = Whole(50 + len(tops), n, 16, dense, g=8)
+    part = n // len(tops)
+    for i, e in enumerate(tops):
+        c.scale[np.unique(c.row(0, np.arange(i * part, n if i + 1 == len(tops) else (i + 1) * part)) // 8)] = 2.0 ** e
+    sm = 2.0 ** (-max(tops) - 10)                        # logits of about 1
+    c.check(*c.run(cuda_device, sm=sm), sm=sm, rows=[0, c.T - 1])
+
+
+@pytest.mark.parametrize("dense", [False, True])
 @pytest.mark.parametrize("order", ["rising", "falling", "both"])
 def test_growing_logits_of_a_whole_list(cuda_device, order, dense):
     """Logits that rise, fall, or rise and fall by far more than a factor of 2^8 per tile."""
