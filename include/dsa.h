@@ -438,8 +438,13 @@ dsa_status dsa_project_append_q8(const dsa_batch *batch, const uint16_t *hidden,
  * the list, evenly spread, so that the sum over many small weights keeps its value: its
  * deviation is at most 2^-8.6 of the values' root mean square, whatever the number of
  * rows (bf16 weights: 2^-9 of each).  The results depend on the inputs alone.  fp32
- * logits, softmax statistics and sums.  A query row with an infinite or NaN entry gives NaN, and so
- * does a selected row with a NaN code.
+ * logits, softmax statistics and sums.  A head whose query has an infinite or NaN entry
+ * gives NaN, and so does every head where a selected row has a NaN code.  Logits
+ * (sm_scale * q.c) beyond fp32's range: a head whose largest one is infinite, either way,
+ * gives NaN; one of negative infinity below finite ones counts as a weight of 0, unless
+ * all of a list's 128 neighbouring entries have one, which may give NaN too.  (Where
+ * sm_scale * scale times the head's largest query entry passes 2^128, even a logit of 0
+ * may.)
  * A row whose scale is outside [2^-100, 2^100] raises DSA_DEV_BAD_SCALE and is
  * skipped.  In the dense form a query position outside its sequence, or well beyond
  * max_kv_len, raises DSA_DEV_BAD_QUERY; such a query, and one with no usable row, gets out = 0 and

@@ -78,6 +78,7 @@ constexpr uint32_t kSCol = 0, kOCol = 256;         // TMEM columns
 constexpr float kTop = 7.f - 8.f;                  // log2 of the largest weights' sum when m is set (see top_sum)
 constexpr float kLimit = 8.9f - 8.f;               // log2 of the weight that makes m move (codes end below 2^8.9)
 constexpr float kStep = 1.f / (1 << 17);           // the smallest step of the weights' codes
+constexpr float kNaN = __builtin_nanf("");
 constexpr int kMaxSplits = 64;
 
 struct Tile {                                      // 128 rows: latent as 4 x 128 B (SW128), RoPE 64 B (SW64)
@@ -509,8 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         };
         // log2 of the sum of four large weights (the largest of each 32 of the group's rows,
         // 1 to 4 times the largest of all) to within 0.75, of head 16 grp + lane mod 16;
-        // infinite where the largest logit is, and -infinity where all are NaN.  red and m
-        // may still hold the last item's sums and references.
+        // not finite where the largest logit is not (or there is none).  red and m may still
+        // hold the last item's sums and references.
+        bool some = false;                          // (a usable row in the tile)
         auto top_sum = [&]() {
           float v[kGH];
 #pragma unroll
@@ -523,11 +525,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
           if (lane == 0) S.top_s[grp][quad] = s_max;
           bad |= !meet(&S.sync[grp], met, lane, p.status, ab);
           const uint32_t(&ts)[4] = S.top_s[grp];
-          far_s = fmaxf(far_s, __uint_as_float(max(max(ts[0], ts[1]), max(ts[2], ts[3]))) * 8.673617e-19f);   // 2^-60
+          const float s_top = __uint_as_float(max(max(ts[0], ts[1]), max(ts[2], ts[3])));
+          far_s = fmaxf(far_s, s_top * 8.673617e-19f);   // 2^-60
+          some = s_top > 0.f;
           const int hl = lane & (kGH - 1);
           const float a0 = S.red[grp][0][hl], a1 = S.red[grp][1][hl], a2 = S.red[grp][2][hl], a3 = S.red[grp][3][hl];
           const float top = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
-          if (fabsf(top) == INFINITY) return top;
+          if (!(fabsf(top) < INFINITY)) return top;
           // whole powers of two above the largest, whose weight then needs no rounding
           return top + rintf(0.25f + lg2_approx((ex2_approx(a0 - top) + ex2_approx(a1 - top)) +
                                                 (ex2_approx(a2 - top) + ex2_approx(a3 - top))));
@@ -545,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         if (!seen) {
           // set the reference at the first usable rows
           const float mx = top_sum();
-          const float up = fabsf(mx) < INFINITY ? mx - kTop : 0.f;
+          // without a finite logit among its rows the head is NaN
+          const float up = fabsf(mx) < INFINITY ? mx - kTop : some ? kNaN : 0.f;
           if ((far = __any_sync(0xffffffffu, usable && s < far_s))) {
             logits(0.f);
 #pragma unroll
@@ -553,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
             shares();
             logits(sg);
           }
-          seen = __any_sync(0xffffffffu, mx > -INFINITY);
+          seen = some;
           if (quad == 0 && lane < kGH) S.m[grp * kGH + lane] = -up;
 #pragma unroll
           for (int i = 0; i < kGH; ++i) x[i] -= __shfl_sync(0xffffffffu, up, i);
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
             // move the reference of the heads that need it, or soon may
             logits(sg);
             const float mx = top_sum();
-            const float up = fabsf(mx) < INFINITY && mx > kTop ? mx - kTop : 0.f;
+            const float up = mx == INFINITY ? kNaN : mx > kTop ? mx - kTop : 0.f;
             // The factor may lie below fp32's range: O, relative to the new weights, is then
             // nothing, but rows of far smaller scales count in l (w / s), which takes it in halves.
             const float half = ex2_approx(-0.5f * up), f = half * half;

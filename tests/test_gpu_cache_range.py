@@ -124,3 +124,66 @@ def test_growing_logits_of_a_whole_list(cuda_device, order, dense):
     q[:, 575] = np.linspace(1, 200, H)
     c.q = np.repeat(inputs.to_bf16_bits(q)[None], c.T, 0)
     c.check(*c.run(cuda_device), rows=[0, c.T - 1])
+
+
+# ------------------------------------------------------------------- logits beyond fp32
+@pytest.mark.parametrize("n,whole", [(100, True), (1000, True), (1000, False)])
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_a_largest_logit_beyond_fp32_gives_nan(cuda_device, n, whole, dense, sign):
+    """Heads whose largest logit passes fp32's range (either way) are NaN; a row far below
+    the others counts nothing; the other heads are as without them."""
+    H = 16
+    if whole:
+        c = Whole(70, n, H, dense)
+    else:
+        c = Case(70, [n], 1, H, 0 if dense else n, 64, 64)
+        if not dense:
+            c.idx[0] = np.arange(n)
+    vals = oracle.e4m3_decode(c.codes)
+    vals[:, 575] = 64.0                                  # of one sign in every row
+    c.codes = inputs.to_e4m3_bytes(vals.astype(np.float32))
+    c.scale[:] = 1.0
+    sm = 1.0 / 24
+    ref = c.run(cuda_device, sm=sm)
+    c.check(*ref, sm=sm, rows=[0])
+    c.q = c.q.copy()
+    beyond = np.zeros((H, 576), np.float32)
+    beyond[:, 575] = sign * 3e38
+    c.q[:, [2, 5]] = inputs.to_bf16_bits(beyond)[None, [2, 5]]
+    out, lse = c.run(cuda_device, sm=sm)
+    nan = np.isnan(oracle.bf16_decode(out))
+    assert nan[:, [2, 5]].all() and np.isnan(lse[:, [2, 5]]).all()
+    rest = [h for h in range(H) if h not in (2, 5)]
+    assert np.array_equal(out[:, rest], ref[0][:, rest]) and np.array_equal(lse[:, rest], ref[1][:, rest])
+
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("at", [0, 500, 999])
+def test_one_logit_beyond_fp32(cuda_device, at, dense, whole):
+    """Above the others in one row of a list it makes its head NaN, below them it takes the
+    row out: the head (all other logits 0) is then the mean of the other rows.
+    Tolerance: half a step of bf16, and 2^-8 of the mean magnitude for weights of 8 bits."""
+    n, H = 1000, 16
+    if whole:
+        c = Whole(71, n, H, dense)
+    else:
+        c = Case(71, [n], 1, H, 0 if dense else n, 64, 64)
+        if not dense:
+            c.idx[0] = np.arange(n)
+    vals = oracle.e4m3_decode(c.codes)
+    vals[:, 575] = 0
+    vals[c.row(0, np.arange(n))[at], 575] = 64.0
+    c.codes = inputs.to_e4m3_bytes(vals.astype(np.float32))
+    c.scale[:] = 1.0
+    q = np.zeros((H, 576), np.float32)
+    q[:, 575] = np.where(np.arange(H) % 2, 3e38, -3e38)
+    c.q = np.repeat(inputs.to_bf16_bits(q)[None], c.T, 0)
+    out, lse = c.run(cuda_device, sm=1.0)
+    got = oracle.bf16_decode(out)
+    assert np.isnan(got[:, 1::2]).all() and np.isnan(lse[:, 1::2]).all()
+    v = np.delete(oracle.e4m3_decode(c.codes[c.row(0, np.arange(n))])[:, :512], at, 0)
+    ref = v.mean(0)
+    assert (np.abs(got[:, 0::2] - ref) <= 2.0 ** -8 * (np.abs(ref) + np.abs(v).mean(0))).all()
+    assert (np.abs(lse[:, 0::2] - np.log(n - 1)) <= 2.0 ** -16).all()
