@@ -273,8 +273,10 @@ __device__ __forceinline__ void item_list(const MlaQ8Params& p, Item& I) {
     I.ok = I.ok && pos >= 0 && pos < I.len && pos < static_cast<int64_t>(p.splits) * p.split_tiles * kRows;
     n = pos + 1;
   }
-  I.e0 = I.sp * p.split_tiles * kRows;
-  I.e1 = I.ok ? min(n, I.e0 + p.split_tiles * kRows) : I.e0;
+  // (a part may reach beyond 2^31 entries: lists of any stated length)
+  const int64_t part = static_cast<int64_t>(p.split_tiles) * kRows, e0 = I.sp * part;
+  I.e0 = static_cast<int>(min(static_cast<int64_t>(n), e0));
+  I.e1 = I.ok ? static_cast<int>(min(static_cast<int64_t>(n), e0 + part)) : I.e0;
 }
 
 // Splits the 64 heads' queries of an item into hi and lo (this warp: heads w0 + 16 i) and

@@ -187,3 +187,20 @@ def test_one_logit_beyond_fp32(cuda_device, at, dense, whole):
     ref = v.mean(0)
     assert (np.abs(got[:, 0::2] - ref) <= 2.0 ** -8 * (np.abs(ref) + np.abs(v).mean(0))).all()
     assert (np.abs(lse[:, 0::2] - np.log(n - 1)) <= 2.0 ** -16).all()
+
+
+@pytest.mark.parametrize("queries", [1, 3, 700])
+def test_any_bound_of_the_lengths(cuda_device, queries):
+    """max_kv_len only has to be no less than any length: the largest number will do, for
+    batches whose lists it cuts into parts and for ones whose lists it leaves whole."""
+    c = Case(80, [700], queries, 16, 0, 64, 0)
+    want = c.run(cuda_device)
+    db = c.batch(cuda_device)
+    db.struct.max_kv_len = 2 ** 31 - 1
+    got = c.run(cuda_device, batch=db)
+    rows = [0, queries // 2, queries - 1]
+    c.check(*want, rows=rows)
+    c.check(*got, rows=rows)
+    if queries > 3:
+        assert B.q8_workspace(B.Q8_MLA, db, H=c.H, k=0, device=cuda_device).numel() == 256
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
