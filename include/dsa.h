@@ -398,7 +398,9 @@ size_t dsa_q8_workspace_size(int op, const dsa_batch *batch, int H_I, int H, int
  *           the first new one) are re-encoded when the scale grows
  *   kv8   = E4M3(kv / scale), round to nearest even, saturating at +-448
  * Scales are thus powers of two: dividing by one is exact, and a re-encoded row
- * loses only what falls below E4M3's smallest step (2^-9 of the scale).
+ * loses only what falls below E4M3's smallest step (2^-9 of the scale).  An earlier scale
+ * may be any number in [2^-100, 2^100] (a cache quantised elsewhere): codes are then those
+ * of the exact quotient kv / scale, and of the exact code * scale / need where the scale grows.
  * Infinite entries saturate, NaN stays NaN.  No other row or scale is written.
  * A token outside its sequence, or a contiguous sequence whose kv_offset is not a
  * multiple of scale_block, raises DSA_DEV_BAD_QUERY and is not appended; one whose

@@ -6,7 +6,8 @@
 // re-encoded when the scale grows), codes = E4M3(kv / scale).  Powers of two make
 // the division exact, so a stored value is rounded once, and re-encoding an
 // earlier row only shifts its exponent (what falls below E4M3's smallest step is
-// rounded again).
+// rounded again).  A block that was quantised elsewhere may hold any scale; its new rows
+// then take a division, rounded once all the same.
 //
 // Bound by memory: 1152 B read and 576 B written per row, once each.  The work is
 // cut into runs: the new rows of one 64-position stretch of one sequence (a page
@@ -46,12 +47,13 @@ constexpr int kCtasPerSm = 3;
 struct QuantSmem {
   uint4 rows[kStretch * kRowBytes / 16];
   uint32_t top[kStretch];                          // largest magnitude (bf16 bits) per scale block of the stretch
-  float inv[kStretch];                             // 1 / its scale
+  float inv[kStretch];                             // 2^-e of its scale's exponent e
   uint64_t full;
 };
 static_assert((sizeof(QuantSmem) + 1024) * kCtasPerSm <= 228 * 1024, "three CTAs share an SM");
 
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+__device__ __forceinline__ int exponent(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }   // x >= 2^-126
 
 // Smallest e in [kMinExp, kMaxExp] with 448 * 2^e >= the bf16 magnitude `bits`
 // (448 = 1.75 * 2^8).
@@ -76,13 +78,42 @@ __device__ __forceinline__ uint32_t encode4(uint32_t a, uint32_t b, float inv) {
          (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3)) << 16);
 }
 
+// A block's earlier scale may be any number, not only a power of two (a cache that was
+// quantised elsewhere).  Quotients and products by one are rounded towards zero with the
+// last bit set where anything was left (`rest`), so that the rounding to E4M3, of far fewer
+// bits, is that of the exact value.  Beyond 512 (and for NaN) it saturates whatever the
+// last bit.
+__device__ __forceinline__ float to_odd(float y, float rest) {
+  return rest != 0.f && fabsf(y) < 512.f ? __uint_as_float(__float_as_uint(y) | 1u) : y;
+}
+// x / m for m in [1, 2).
+__device__ __forceinline__ float quotient(float x, float m) {
+  const float y = __fdiv_rz(x, m);
+  return to_odd(y, fmaf(-y, m, x));
+}
+__device__ __forceinline__ float product(float x, float f) {
+  const float y = __fmul_rz(x, f);
+  return to_odd(y, fmaf(x, f, -y));
+}
+
+// encode4 by any scale: inv = 2^-e and m = scale * 2^-e.
+__device__ __noinline__ uint32_t encode4_any(uint32_t a, uint32_t b, float inv, float m) {
+  const float2 x = make_float2(quotient(__uint_as_float(a << 16) * inv, m),
+                               quotient(__uint_as_float(a & 0xffff0000u) * inv, m));
+  const float2 y = make_float2(quotient(__uint_as_float(b << 16) * inv, m),
+                               quotient(__uint_as_float(b & 0xffff0000u) * inv, m));
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3)) |
+         (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3)) << 16);
+}
+
 __device__ __forceinline__ uint32_t reencode4(uint32_t v, float f) {
   uint32_t r = 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v >> (16 * h)), __NV_E4M3);
     const float2 y = __half22float2(__half2(x));
-    r |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(y.x * f, y.y * f), __NV_SATFINITE, __NV_E4M3))
+    r |= static_cast<uint32_t>(
+             __nv_cvt_float2_to_fp8x2(make_float2(product(y.x, f), product(y.y, f)), __NV_SATFINITE, __NV_E4M3))
          << (16 * h);
   }
   return r;
@@ -227,7 +258,7 @@ __global__ void __launch_bounds__(kQuantThreads, kCtasPerSm) quantize_append_ker
     if (tid >= b0 && tid <= last) {
       const float s = tid == b0 ? s0 : pow2f(need_exp(S.top[tid]));
       p.scale[blk + tid - b0] = s;
-      S.inv[tid] = 1.f / s;
+      S.inv[tid] = pow2f(-exponent(s));
     }
     // earlier rows of the first block, when its scale grows
     if (s_ok && s0 > s_old) {
@@ -243,9 +274,18 @@ __global__ void __launch_bounds__(kQuantThreads, kCtasPerSm) quantize_append_ker
       }
     }
     __syncthreads();
+    // rows of the first block, where its scale is no power of two
+    const int any = s0 != pow2f(exponent(s0)) ? min(n, ((b0 + 1) << gl) - first) : 0;
+    if (any) {
+      const float inv = S.inv[b0], m = s0 * inv;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(S.rows);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.kv8 + row * DSA_D_QK);
+      for (int c = tid; c < any * (DSA_D_QK / 4); c += kQuantThreads)
+        dst[c] = encode4_any(src[2 * c], src[2 * c + 1], inv, m);
+    }
     // codes of the new rows, 16 per thread and step
     uint4* out = reinterpret_cast<uint4*>(p.kv8 + row * DSA_D_QK);
-    for (int c = tid; c < n * kPieces; c += kQuantThreads) {
+    for (int c = any * kPieces + tid; c < n * kPieces; c += kQuantThreads) {
       const float inv = S.inv[(first + c / kPieces) >> gl];
       const uint4 a = S.rows[2 * c], b = S.rows[2 * c + 1];
       out[c] = make_uint4(encode4(a.x, a.y, inv), encode4(a.z, a.w, inv), encode4(b.x, b.y, inv),

@@ -204,3 +204,55 @@ def test_any_bound_of_the_lengths(cuda_device, queries):
     if queries > 3:
         assert B.q8_workspace(B.Q8_MLA, db, H=c.H, k=0, device=cuda_device).numel() == 256
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------- appends to scales that are not powers of two
+@pytest.mark.parametrize("g", [2, 16, 64])
+@pytest.mark.parametrize("T", [3, 4000])
+def test_append_into_blocks_of_any_scale(cuda_device, g, T):
+    """A block's earlier scale may be any number in range (a cache quantised elsewhere): new
+    codes are E4M3 of the exact quotient, and re-encoded ones of the exact product."""
+    from oracle import cache as C
+    from tests.test_gpu_cache import _append, _same_codes
+    r = np.random.default_rng(g + T)
+    per = -(-T // 60)
+    n = -(-T // per)
+    old = r.integers(1, 70, n)
+    new = np.minimum(r.integers(1, per + 1, n), per)
+    c = Case(90 + g, [int(x) for x in old + new], 1, 8, 0, g, 64)
+    c.scale = (2.0 ** r.integers(-8, 6, c.scale.size) * r.uniform(1, 2, c.scale.size)).astype(np.float32)
+    q_seq = np.repeat(np.arange(n), new)
+    q_pos = np.concatenate([np.arange(o, o + m) for o, m in zip(old, new)])
+    kv = oracle.bf16_decode(inputs.to_bf16_bits((r.standard_normal((q_seq.size, 576))
+                                                 * np.exp2(r.integers(-3, 8, (q_seq.size, 1)))).astype(np.float32)))
+    # quotients next to E4M3's ties: the scale of every other sequence's block is an entry over a tie
+    for s in range(0, n, 2):
+        b = int(c.row(s, int(old[s]))) // g
+        tie = (2 * r.integers(8, 16) + 1) / 2.0 * 2.0 ** r.integers(-4, 4)
+        x = max(abs(kv[int(np.flatnonzero(q_seq == s)[0]), 5]), 2.0 ** -6)
+        c.scale[b] = np.float32(x / tie)
+    bits = inputs.to_bf16_bits(kv.astype(np.float32))
+    codes, scale = _append(cuda_device, c, bits, q_seq, q_pos)
+    want = C.quantize_append(c.codes, c.scale, g, oracle.bf16_decode(bits), q_seq, q_pos, lambda s, p: int(c.row(s, p)))
+    assert np.array_equal(scale, want[1].astype(np.float32)) and _same_codes(codes, want[0])
+
+
+@pytest.mark.parametrize("exp", [-100, -60, 0, 60, 99])
+def test_append_into_blocks_of_any_scale_at_the_ends(cuda_device, exp):
+    """The same at the smallest and largest scales, with entries of every size, infinite
+    ones and NaN among the new rows."""
+    from oracle import cache as C
+    from tests.test_gpu_cache import _append, _same_codes
+    r = np.random.default_rng(exp + 200)
+    g, n = 16, 40
+    c = Case(95, [16] * n, 1, 8, 0, g, 64)
+    c.scale = (2.0 ** float(exp) * r.uniform(1, 2, c.scale.size)).astype(np.float32)
+    q_seq, q_pos = np.repeat(np.arange(n), 3), np.tile([5, 6, 7], n)
+    size = np.clip(exp + r.integers(-14, 9 if exp < 99 else 5, (q_seq.size, 1)) + r.integers(-2, 3, (q_seq.size, 576)), -132, 126)
+    kv = (r.standard_normal((q_seq.size, 576)) * np.exp2(size.astype(float))).astype(np.float32)
+    kv[::7, 3], kv[1::7, 4], kv[2::7, 5] = np.inf, -np.inf, np.nan
+    kv[3::7, 6:9] = [0.0, -0.0, 1e-40]
+    bits = inputs.to_bf16_bits(kv)
+    codes, scale = _append(cuda_device, c, bits, q_seq, q_pos)
+    want = C.quantize_append(c.codes, c.scale, g, oracle.bf16_decode(bits), q_seq, q_pos, lambda s, p: int(c.row(s, p)))
+    assert np.array_equal(scale, want[1].astype(np.float32)) and _same_codes(codes, want[0])
