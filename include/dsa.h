@@ -108,6 +108,9 @@ typedef struct dsa_batch {
  * Bytes of workspace `ws` an operation needs (always >= 256: the status word and
  * a small plan live at its start).  `ld` is the score row stride (elements) for
  * DSA_OP_FORWARD (0 = the default, max_kv_len rounded up to a multiple of 4).
+ * The size does not grow with the batch throughout: few queries are cut into parts, whose
+ * partial results need room that many do not.  A workspace for batches of several sizes
+ * takes the largest of their sizes.
  * Returns 0 for an invalid op or batch.
  */
 size_t dsa_workspace_size(int op, const dsa_batch *batch, int H_I, int H, int k, int64_t ld);
@@ -380,6 +383,8 @@ uint64_t dsa_launch_count(void);
 
 /* Bytes of workspace an 8-bit-cache operation needs (>= 256: the status word lies
  * at its start).  k = 0 with DSA_Q8_MLA asks for the dense form (idx = NULL).
+ * As with dsa_workspace_size a smaller batch may need more than a larger one (one query
+ * of 2048 rows 4 MB, 4096 of them 256 bytes).
  * Returns 0 for an invalid op, batch, H_I, H or k.  H_I is read by
  * DSA_Q8_FORWARD and DSA_Q8_PROJECT, H by all but DSA_Q8_APPEND. */
 size_t dsa_q8_workspace_size(int op, const dsa_batch *batch, int H_I, int H, int k);

@@ -1,16 +1,19 @@
 // Pages of a paged cache on sm_100a: growing, cutting and freeing sequences with
 // copy on write, forks, compaction.  Integer bookkeeping plus copies of whole
 // pages; the results are those of the sequential definition in the header
-// whatever order the threads run in (lists are ranked by prefix sums; atomics
-// only add, or take a maximum of list positions).
+// whatever order the threads run in: lists are ranked by prefix sums; atomics add, or
+// take a minimum or maximum of list positions.  Which slot of a resize's hash table a
+// sequence claims depends on the order, but not what the slot comes to hold (the lowest
+// entry that names it), and only that is read.
 //
 // Bound by latency for the bookkeeping (a few dependent passes over lists of some
 // hundred entries and the reference counts), so the kernels of a call are launched
 // with programmatic dependent launch: each is resident, with its lists read, when
 // the one before it ends.  The copies are bound by memory (each byte read and
 // written once): many small chunks in flight per SM.
-// Measured: fork of 24 sequences 8.1 us a call (3.3 on the device), of 192 8.2; compaction
-// of 4096 pages (46 MB to move) 18.5 us, of 32768 (372 MB) 139 us, 5.3 TB/s; resizes below.
+// Measured, a call on a stream and on the device: fork of 24 sequences 8.6 and 3.9 us, of
+// 192 8.5 and 6.4; compaction of 4096 pages (46 MB to move) 22.6 and 17.1 us, of 32768
+// (372 MB) 142 and 139 us, 5.3 TB/s; resizes below.
 #include <atomic>
 #include <climits>
 
@@ -108,7 +111,7 @@ __device__ __forceinline__ int owner_of(const int32_t* start, int n, int k) {
 // where the kernel before has copied them.  Bound by latency: some 25 dependent steps.
 // On the device, with and without kOwn: 256 entries that drop 3500 and take 2800 of 24576
 // pages 20.0 and 22.8 us; 64 entries of a decode step 8.8 and 7.9 us, but a launch more
-// on the host (11 us a call against 13).
+// on the host (12 us a call against 13).
 template <bool kOwn>
 __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesParams p) {
   extern __shared__ __align__(16) int32_t own_ref[];   // kOwn: [num_pages]

@@ -17,10 +17,10 @@
 // once; three CTAs per SM keep some 200 KB in flight.  Long token lists (prompts) are
 // first searched for the places where runs begin; in short ones (decode steps, where
 // nearly every token is a run) each token has its own CTA.
-// Measured: 61,000 prompt tokens in blocks of 64, 31 us with both kernels (106 MB, 3.4
+// Measured on the device: 61,000 prompt tokens in blocks of 64, 32 us with both kernels (106 MB, 3.3
 // TB/s, half of a copy's rate): the 950 runs go round the 444 CTAs 2.2 times, so that the
 // last round is nearly empty, and a CTA's copy, maxima and codes follow one another.  A
-// decode step of 128 tokens, 6.2 us on the device, is launch and latency.  With and
+// decode step of 128 tokens, 6.5 us, is launch and latency.  With and
 // without the search: 128 tokens in twos 8.2 and 6.2 us, 1024 in twos 10.3 and 8.2, 2000 of
 // a prompt 10.3 and 10.5, 4000 10.3 and 14.3.
 #include <cuda_fp16.h>

@@ -35,12 +35,14 @@
 // goes by quarters of 32 rows (one K step, all dims, lo and hi), each of which gives
 // its rows and weights back, so the next tile's rows and weights follow it closely.
 // Bound by the chain through the two row tiles: a tile's rows, S^T, weights and O^T take
-// some 8,800 clocks and the tensor work in them 2,850, so a tile takes 4,300 to 4,800
-// (ncu: tensor pipe 40%, issue slots 52%, DRAM 6%); beside them an item costs some 10,000
-// (the queries' split 6,000, first rows, output).  A third row tile does not fit beside
-// the queries.  Measured: 4096 queries, 128 heads, 2048 rows each, 2.77 ms (843 TFLOP/s of
-// the bf16 product's work, at 1.58 GHz under the power cap); 64 contexts of 2048 selected
-// rows 57 us; 24 ragged contexts of 1 .. 8191 rows, dense, 60 us; one query 18.5 us.
+// some 8,800 clocks and the tensor work in them 2,850, so a tile takes 4,300 to 4,800;
+// beside them an item costs some 10,000 (the queries' split 6,000, first rows, output).
+// A third row tile does not fit beside the queries.  Near its limit is the shared-memory
+// port: the products read 344 KB of operands per tile (ncu: 48% of its clocks), loads,
+// stores and gathers take 32% (tensor pipe 39%, issue slots 51%, DRAM 7%).
+// Measured on the device: 4096 queries, 128 heads, 2048 rows each, 2.76 to 2.83 ms (846 to
+// 825 TFLOP/s of the bf16 product's work, under the power cap); 64 contexts of 2048 selected
+// rows 59 us; 24 ragged contexts of 1 .. 8191 rows, dense, 61 to 67 us; one query 18.5 us.
 //
 // 32 warps: 0-15 softmax (warp w: rows 32 (w mod 4) .., 16 heads) and, between items,
 // the next queries' hi/lo split, 16-23 row gathers (16-byte cp.async), 24-27 the
@@ -436,9 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_q8_kernel(MlaQ8Params p) {
         ++nq;
       }
       if (grp * kGH >= p.H) {
-        // Never a head for the group: its columns of W and O are not looked at (16 heads, 740
-        // queries of a prompt 223 -> 207 us).  Skipping the empty groups of a second part of
-        // the heads as well took 72 heads from 452 to 487 us.
+        // Never a head for the group: its columns of W and O are not looked at (16 heads, on
+        // the device: 740 queries of a prompt 211 us, 233 without this; 64 sequences 36.9 and
+        // 38.4).  With the empty groups of a second part of the heads skipped as well, 740
+        // queries of 72 heads took 499 us instead of 466.
         for (int j = 0; j < tiles; ++j, ++g) {
           const int b = g & 1;
           bad |= !wait(&S.s_full[b], (g >> 1) & 1, p.status, ab);
@@ -1030,9 +1033,9 @@ __device__ __forceinline__ float4 load_if(const float* at, bool take) {
 // A CTA per query and head, four dims per thread.  Every warp works the weights out for
 // itself (lane i: parts i and 32 + i).  Parts of weight 0 may never have been written.
 // With few CTAs (kEager) latency counts: 16 parts are read while the weights are worked
-// out, whatever those turn out to be (one query of 16 parts 18.5 us in all, against 20.5
-// the other way).  With many, only parts with a weight are read, eight at a time (24
-// ragged contexts of 128 heads 61 us in all against 64).
+// out, whatever those turn out to be (one query of 16 parts 18.7 us on the device with the
+// attention, against 20.7 the other way).  With many, only parts with a weight are read,
+// eight at a time (24 ragged contexts of 128 heads 60.7 us against 66.2).
 template <bool kEager>
 __global__ void __launch_bounds__(128) combine_kernel(MlaQ8Params p) {
   const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
@@ -1118,7 +1121,7 @@ static cudaError_t prepare_device(size_t smem) {
 // three tiles' time beside its tiles (the first row latencies, the first reference,
 // the output).  Where the items go round once, the time is that of one item;
 // otherwise that of an even share, and one item at the end: 24 contexts of 1 .. 8191
-// rows, dense, take 60 us in the parts of 12 tiles chosen here and 68 us in parts of 20
+// rows, dense, took 60 us in the parts of 12 tiles chosen here and 68 us in parts of 20
 // that go round once.  Lists of 16 tiles that go round more than once are left whole:
 // 75 queries of 128 heads 95 us, in halves 98; 149 queries 140 us, in halves 163.
 int mla_q8_plan(int T, int H, int64_t most, int64_t mean, int sms, int* split_tiles) {
