@@ -440,11 +440,12 @@ dsa_status dsa_project_append_q8(const dsa_batch *batch, const uint16_t *hidden,
  * the softmax weights (times their rows' scales) enter as sums of two E4M3 numbers,
  * which hold 8 significant bits like bf16 down to 2^-8 of the largest entry of the
  * query's head (queries; an absolute error of 2^-17 of that entry below) and to 2^-7 of
- * the largest p_i * scale_i (weights; steps of 2^-14 of it below).  A weight smaller than
- * its step is taken up to the step or down to 0 by an offset that goes by its place in
- * the list, evenly spread, so that the sum over many small weights keeps its value: its
- * deviation is at most 2^-8.6 of the values' root mean square, whatever the number of
- * rows (bf16 weights: 2^-9 of each).  The results depend on the inputs alone.  fp32
+ * the largest p_i * scale_i (weights; steps of 2^-14 of it below, so that a block whose
+ * scale is 2^n times the others' makes their rows' steps 2^n coarser).  A weight smaller
+ * than its step is taken up to the step or down to 0 by an offset that goes by its place in
+ * the list, evenly spread, so that the sum over many small weights keeps its value: with
+ * equal scales its deviation is at most 2^-8.6 of the values' root mean square, whatever
+ * the number of rows (bf16 weights: 2^-9 of each).  The results depend on the inputs alone.  fp32
  * logits, softmax statistics and sums.  A head whose query has an infinite or NaN entry
  * gives NaN, and so does every head where a selected row has a NaN code.  Logits
  * (sm_scale * q.c) beyond fp32's range: a head whose largest one is infinite, either way,

@@ -24,7 +24,7 @@
 // sum of many keeps its value: its deviation is at most 2^-8.6 of the values' size and does
 // not grow with the list.  (Rounding to nearest, with the largest at 2^5, lost 3% of the
 // output beside a weight of 0.8 over 8191 rows and 12% over 32768.  The offsets cost the
-// prefill of 4096 queries 2%.  A largest weight of 2^7 throughout is as exact, but the
+// prefill of 4096 queries 3%.  A largest weight of 2^7 throughout is as exact, but the
 // reference then moves in most lists: 3290 us against 2740.)
 //
 // One CTA per SM works through items (query, 64 heads, split of the row list), the

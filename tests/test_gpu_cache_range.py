@@ -126,6 +126,24 @@ def test_growing_logits_of_a_whole_list(cuda_device, order, dense):
     c.check(*c.run(cuda_device), rows=[0, c.T - 1])
 
 
+@pytest.mark.parametrize("first,then", [(0, 1), (127, 0), (128, 300), (300, 2), (999, 0)])
+@pytest.mark.parametrize("dense", [False, True])
+def test_tiles_without_usable_rows_in_a_whole_list(cuda_device, first, then, dense):
+    """The first rows, and every other tile after them, cannot be used (empty slots, or
+    scales that are none): the reference is set by the first tile that has one."""
+    n = 1000
+    c = Whole(65, n, 24, dense, g=1)
+    off = np.arange(n) < first
+    off |= (np.arange(n) // 128 % 2 == 1) & (np.arange(n) % 128 >= then % 128) & (np.arange(n) != n - 1)
+    if dense:
+        c.scale[c.row(0, np.flatnonzero(off))] = 0.0
+        skip = c.scale == 0
+        c.check(*c.run(cuda_device, flags=B.DEV_BAD_SCALE if off.any() else 0), rows=[0, c.T - 1], skip=skip)
+    else:
+        c.idx[:, off] = -1
+        c.check(*c.run(cuda_device), rows=[0, c.T - 1])
+
+
 # ------------------------------------------------------------------- logits beyond fp32
 @pytest.mark.parametrize("n,whole", [(100, True), (1000, True), (1000, False)])
 @pytest.mark.parametrize("dense", [False, True])
